@@ -348,6 +348,71 @@ gdn_status gdn_chunk_fwd_noalloc(const gdn_shape *shape, const void *q, const vo
                                  const void *v, const float *g, const float *beta,
                                  const float *h0, void *o, float *h_T, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * A pool of recurrent states, for serving.  state [n_slots, H_v, d_k, d_v]
+ * fp32 holds one state per slot and value head; row b of a call works on the
+ * state in slot slots[b].
+ *   B        rows
+ *   n        tokens per row: 1 for gdn_step, the tree's nodes (1..64) else
+ *   H_qk, H_v, d_k, d_v, dtype, o_dtype   as in gdn_shape
+ *   n_slots  slots of the pool
+ *   g_fixed  0: log decays per token, g [B, n, H_v]; 1: one per value head,
+ *            g [H_v]
+ * slots [B] int32 DEVICE array, or NULL: row b has slot b (n_slots >= B).
+ * A row whose slot is outside [0, n_slots) (a padded batch marks such rows
+ * with -1) has no state: its outputs are zero and no state is written.  Rows
+ * of one call that write states and name the same slot: the first one is
+ * run, the others are treated as rows without a state.  States that no row
+ * names are left as they are.
+ * The rule is the gated delta rule at the top of this file, or, with
+ * beta = NULL, linear attention with a decay per head (the same rule without
+ * the correction):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = S_t^T q_t.
+ * B * H_v <= 2^26.  No workspace is used. */
+typedef struct {
+  int32_t B, n, H_qk, H_v, d_k, d_v, n_slots, g_fixed;
+  int32_t dtype, o_dtype;
+} gdn_pool_shape;
+
+/* One token of every row: the recurrent form of gdn_chunk_fwd (and of
+ * gdn_linear_fwd) for decoding.  Each row's state is advanced in place and
+ * read with q.
+ *   q, k [B, H_qk, d_k], v [B, H_v, d_v] dtype; g [B, H_v] or [H_v] fp32;
+ *   beta [B, H_v] fp32 or NULL (the linear rule); state: the pool (read and
+ *   written); o [B, H_v, d_v] o_dtype (written).  shape->n must be 1. */
+gdn_status gdn_step(const gdn_pool_shape *shape, const void *q, const void *k, const void *v,
+                    const float *g, const float *beta, const int32_t *slots, float *state, void *o,
+                    void *hip_stream);
+
+/* The check of a tree of drafted tokens: node r of a row continues node
+ * parents[r] (its state is the rule applied to that node's state), or the
+ * row's state in the pool for parents[r] = -1.  Nodes are numbered with
+ * ancestors first (parents[r] < r); a node with any other value of parents,
+ * or with an ancestor that has one, is absent: its outputs are zero, its
+ * inputs are not read into any result.  The pool is only read, so rows may
+ * share a slot (drafts forked from one sequence).
+ *   q, k [B, n, H_qk, d_k], v [B, n, H_v, d_v] dtype; g [B, n, H_v] or [H_v],
+ *   beta [B, n, H_v] fp32 or NULL (the linear rule); parents [B, n] int32;
+ *   o [B, n, H_v, d_v] o_dtype, u [B, n, H_v, d_v] fp32 (written): u are the
+ *   values that the nodes write, beta (v - (e^g S)^T k) (v itself for the
+ *   linear rule), for gdn_tree_commit. */
+gdn_status gdn_tree_fwd(const gdn_pool_shape *shape, const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, const int32_t *parents,
+                        const int32_t *slots, const float *state, void *o, float *u,
+                        void *hip_stream);
+
+/* The commit of an accepted path: row b's state becomes the state of node
+ * last[b] (every node from the root to it applied in order), in place:
+ *     S' = e^{G_a} S + sum over the path's nodes i of e^{G_a - G_i} k_i u_i^T,
+ * a = last[b], G the sum of the log decays along a node's path, u from
+ * gdn_tree_fwd (same k, g, parents).  last[b] outside [0, n) (nothing was
+ * accepted) or an absent node leaves the row's state as it is.
+ *   k [B, n, H_qk, d_k] dtype, u [B, n, H_v, d_v] fp32, g as above, parents
+ *   [B, n], last [B] int32.  shape->o_dtype is not used. */
+gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const float *u,
+                           const float *g, const int32_t *parents, const int32_t *last,
+                           const int32_t *slots, float *state, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

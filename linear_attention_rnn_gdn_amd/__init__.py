@@ -12,6 +12,10 @@ Functions (same names as the C entry points, without the ``gdn_`` prefix):
   compose_prefix(A, Bm, h_init=None, split_bf16=False)          -> (h_in, h_final)
   chunk_transform(k, v, g, beta, chunk=128, want_T=False)       -> (G, T, W, U)
   workspace_size(...), validate(...)
+States in a pool [n_slots,H_v,d_k,d_v], for serving (beta=None: the linear rule):
+  step(q, k, v, g, beta, state, slots=None)                     -> o
+  tree_fwd(q, k, v, g, beta, parents, state, slots=None)        -> (o, u)
+  tree_commit(k, u, g, parents, last, state, slots=None)        -> state
 """
 from __future__ import annotations
 
@@ -35,6 +39,11 @@ class GdnShape(ctypes.Structure):
                 ("B", "T", "H_qk", "H_v", "d_k", "d_v", "chunk", "n_groups", "dtype", "o_dtype")]
 
 
+class GdnPoolShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "n", "H_qk", "H_v", "d_k", "d_v", "n_slots", "g_fixed", "dtype", "o_dtype")]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS.get(status, status)} (status {status})")
@@ -47,7 +56,8 @@ SYMBOLS = ("gdn_status_str", "gdn_validate", "gdn_workspace_size", "gdn_workspac
            "gdn_chunk_fwd", "gdn_chunk_fwd_varlen",
            "gdn_chunk_fwd_stages", "gdn_chunk_fwd_timed", "gdn_chunk_fold", "gdn_compose_prefix",
            "gdn_chunk_transform", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_affine",
-           "gdn_workspace_size_bwd", "gdn_chunk_bwd_state", "gdn_workspace_size_bwd_grads", "gdn_chunk_bwd")
+           "gdn_workspace_size_bwd", "gdn_chunk_bwd_state", "gdn_workspace_size_bwd_grads", "gdn_chunk_bwd",
+           "gdn_step", "gdn_tree_fwd", "gdn_tree_commit")
 STAGE_PREP, STAGE_FOLD, STAGE_PREFIX, STAGE_WALK, STAGE_OUT, STAGE_ALL = 1, 2, 4, 8, 16, 31
 
 
@@ -95,6 +105,13 @@ def lib():
         L.gdn_workspace_size_bwd_grads.restype = I
         L.gdn_chunk_bwd.argtypes = [SP] + [P] * 15 + [SZ, P]
         L.gdn_chunk_bwd.restype = I
+        PP = ctypes.POINTER(GdnPoolShape)
+        L.gdn_step.argtypes = [PP] + [P] * 9
+        L.gdn_step.restype = I
+        L.gdn_tree_fwd.argtypes = [PP] + [P] * 11
+        L.gdn_tree_fwd.restype = I
+        L.gdn_tree_commit.argtypes = [PP] + [P] * 8
+        L.gdn_tree_commit.restype = I
         _lib = L
     return _lib
 
@@ -415,3 +432,136 @@ def chunk_transform(k, v, g, beta, chunk=128, want_T=False, stream=None):
                                    _ptr(G), _ptr(Tm), _ptr(W), _ptr(U), _stream(stream))
     _check(st, "gdn_chunk_transform")
     return G, Tm, W, U
+
+
+# ---------------------------------------------------------------------------
+# states in a pool: the single-token step, drafted trees
+
+
+class _On:
+    """The stream a call goes to: ``stream``, or the current stream of the
+    tensors' device (which is made current for the launch).  Outputs and
+    workspace allocated inside belong to that stream."""
+    __slots__ = ("handle", "_stack")
+
+    def __init__(self, dev, stream):
+        self._stack = []
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+            self._stack.append(torch.cuda.stream(stream))
+        elif torch.cuda.current_device() != dev.index:
+            self._stack.append(torch.cuda.device(dev))
+        self.handle = stream
+
+    def __enter__(self):
+        for c in self._stack:
+            c.__enter__()
+        return (torch.cuda.current_stream() if self.handle is None else self.handle).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._stack):
+            c.__exit__(*exc)
+
+
+def _check_tensors(dev, *items):
+    """Each item: (tensor, name, dtype, shape); raises what _need raises."""
+    for t, name, dtype, shape in items:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.device == dev and t.is_cuda):
+            _need(t, name, dtype, shape, dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pool_dims(k, Hv_of, state, slots, lead):
+    """Sizes of a call on a pool: checks k and the pool; ``lead``: leading
+    dimensions before the heads (1: rows, 2: rows and nodes)."""
+    if not isinstance(k, torch.Tensor) or not isinstance(Hv_of, torch.Tensor) or not isinstance(state, torch.Tensor):
+        raise TypeError("k, v (u) and state must be tensors")
+    if k.dim() != lead + 2 or Hv_of.dim() != lead + 2 or state.dim() != 4:
+        raise ValueError(f"k and v (u) must have {lead + 2} dimensions and state 4")
+    _dt(k.dtype)
+    B, n = k.shape[0], (k.shape[1] if lead == 2 else 1)
+    Hqk, dk = k.shape[-2:]
+    Hv, dv = Hv_of.shape[-2:]
+    dev = k.device
+    _check_tensors(dev, (k, "k", k.dtype, k.shape), (state, "state", torch.float32, (state.shape[0], Hv, dk, dv)))
+    if slots is not None:
+        _check_tensors(dev, (slots, "slots", torch.int32, (B,)))
+    return B, n, Hqk, Hv, dk, dv, state.shape[0], dev
+
+
+def _decay_shape(g, per_token):
+    return (1, per_token[-1:]) if isinstance(g, torch.Tensor) and g.dim() == 1 else (0, per_token)
+
+
+def step(q, k, v, g, beta, state, slots=None, o_dtype=torch.float32, out=None, stream=None):
+    """One token of every row (gdn_step): the recurrent form, for decoding.
+
+    q, k [B,H_qk,d_k]; v [B,H_v,d_v] (bf16 or fp32); g [B,H_v] or [H_v] fp32;
+    beta [B,H_v] fp32, or None for the linear rule (S = e^g S + k v^T); state
+    [n_slots,H_v,d_k,d_v] fp32, advanced in place; slots [B] int32 on the
+    device (None: row b has slot b).  A row whose slot is outside the pool,
+    or is an earlier row's slot, gets a zero output and writes no state.
+    Returns o [B,H_v,d_v] o_dtype."""
+    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, v, state, slots, 1)
+    fixed, gshape = _decay_shape(g, (B, Hv))
+    _check_tensors(dev, (q, "q", k.dtype, (B, Hqk, dk)), (v, "v", k.dtype, (B, Hv, dv)), (g, "g", torch.float32, gshape))
+    if beta is not None:
+        _check_tensors(dev, (beta, "beta", torch.float32, (B, Hv)))
+    if out is not None:
+        _check_tensors(dev, (out, "o", o_dtype, (B, Hv, dv)))
+    shape = GdnPoolShape(B, 1, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
+    with _On(dev, stream) as st:
+        o = out if out is not None else torch.empty((B, Hv, dv), dtype=o_dtype, device=dev)
+        _check(lib().gdn_step(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(slots), _addr(state),
+                              _addr(o), st), "gdn_step")
+    return o
+
+
+def tree_fwd(q, k, v, g, beta, parents, state, slots=None, o_dtype=torch.float32, out=None, values=None, stream=None):
+    """The check of a tree of drafted tokens (gdn_tree_fwd): every node's
+    output from its parent's state; the pool is only read.
+
+    q, k [B,n,H_qk,d_k]; v [B,n,H_v,d_v]; g [B,n,H_v] or [H_v] fp32; beta
+    [B,n,H_v] fp32 or None (the linear rule); parents [B,n] int32: an earlier
+    node, or -1 for the row's state (any other value: an absent node, zero
+    outputs); n <= 64; state [n_slots,H_v,d_k,d_v] fp32; slots as in step (rows
+    may share a slot).  Returns (o [B,n,H_v,d_v] o_dtype, u [B,n,H_v,d_v] fp32,
+    the values the nodes write, for tree_commit)."""
+    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, v, state, slots, 2)
+    fixed, gshape = _decay_shape(g, (B, n, Hv))
+    _check_tensors(dev, (q, "q", k.dtype, (B, n, Hqk, dk)), (v, "v", k.dtype, (B, n, Hv, dv)),
+                   (g, "g", torch.float32, gshape), (parents, "parents", torch.int32, (B, n)))
+    if beta is not None:
+        _check_tensors(dev, (beta, "beta", torch.float32, (B, n, Hv)))
+    if out is not None:
+        _check_tensors(dev, (out, "o", o_dtype, (B, n, Hv, dv)))
+    if values is not None:
+        _check_tensors(dev, (values, "u", torch.float32, (B, n, Hv, dv)))
+    shape = GdnPoolShape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
+    with _On(dev, stream) as st:
+        o = out if out is not None else torch.empty((B, n, Hv, dv), dtype=o_dtype, device=dev)
+        u = values if values is not None else torch.empty((B, n, Hv, dv), dtype=torch.float32, device=dev)
+        _check(lib().gdn_tree_fwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(parents),
+                                  _addr(slots), _addr(state), _addr(o), _addr(u), st), "gdn_tree_fwd")
+    return o, u
+
+
+def tree_commit(k, u, g, parents, last, state, slots=None, stream=None):
+    """The commit of an accepted path (gdn_tree_commit): row b's state becomes
+    the state of node last[b], in place (last[b] outside the tree: left as it
+    is).  k, g, parents as given to tree_fwd, u as returned by it; last [B]
+    int32.  Rows naming one slot: the first is run.  Returns state."""
+    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, u, state, slots, 2)
+    fixed, gshape = _decay_shape(g, (B, n, Hv))
+    _check_tensors(dev, (u, "u", torch.float32, (B, n, Hv, dv)), (g, "g", torch.float32, gshape),
+                   (parents, "parents", torch.int32, (B, n)), (last, "last", torch.int32, (B,)))
+    shape = GdnPoolShape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), F32)
+    with _On(dev, stream) as st:
+        _check(lib().gdn_tree_commit(shape, _addr(k), _addr(u), _addr(g), _addr(parents), _addr(last), _addr(slots),
+                                     _addr(state), st), "gdn_tree_commit")
+    return state

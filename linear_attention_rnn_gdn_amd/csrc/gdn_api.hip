@@ -14,14 +14,12 @@
 
 #include "gdn.h"
 #include "gdn_bwd.h"
+#include "gdn_host.h"
 #include "gdn_kernels.h"
 
 using namespace gdn;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
   size_t G, W, Kt, U, Hs, Vn, A, Bp, Hin, Ct, Jt, Nt, total;
@@ -96,18 +94,6 @@ Layout layout_n(const gdn_shape &s, size_t rows, size_t N, size_t nseq, bool han
 }
 Layout layout(const gdn_shape &s) { return layout_n(s, s.B, chunks_of(s), 0, !fused_walk(s)); }
 Layout layout_varlen(const gdn_shape &s) { return layout_n(s, 1, varlen_nmax(s), s.B); }
-
-bool misaligned(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
-
-gdn_status check_launch() {
-  return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
-}
-
-#define GDN_TRY(x)                       \
-  do {                                   \
-    gdn_status st_ = (x);                \
-    if (st_ != GDN_OK) return st_;       \
-  } while (0)
 
 // copies h0 (or zero) to h_T for an empty sequence
 __global__ void copy_state_kernel(const float *src, float *dst, size_t n) {

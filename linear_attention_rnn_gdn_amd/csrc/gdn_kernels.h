@@ -65,11 +65,11 @@
 #pragma once
 #include <type_traits>
 
+#include "gdn_common.h"
 #include "gdn_mfma.h"
 
 namespace gdn {
 
-constexpr int D = 128;        // d_k = d_v
 constexpr int NT = 256;       // threads per workgroup
 // walk kinds: WALK (the state h from h0; hands h and V' to the output stage),
 // FOLD (the augmented state [A | B] of a group from [I | 0]: the group's
@@ -101,19 +101,6 @@ template <int MODE> struct Prec {
   static constexpr int h_store = MODE == MODE_F32 ? ST_F32 : ST_SPLIT;
   static constexpr int v_store = MODE == MODE_F32 ? ST_F32 : ST_SPLIT;
 };
-
-// 1-D workgroup index -> (unit, part) with the `parts` workgroups of a unit on
-// one XCD (falls back to unit-major order when units is not a multiple of 8).
-__device__ __forceinline__ void xcd_unit(int L, int parts, int units, int &unit, int &part) {
-  if ((units & 7) == 0) {
-    const int x = L & 7, i = L >> 3;
-    unit = (i / parts) * 8 + x;
-    part = i % parts;
-  } else {
-    unit = L / parts;
-    part = L % parts;
-  }
-}
 
 // Store a wave's column of result tiles (rows 16m + 4g + i, column lr) for the
 // output stage, at `dst` (this chunk's and slice's part of the tensor).  bf16

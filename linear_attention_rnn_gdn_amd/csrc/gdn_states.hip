@@ -1,0 +1,143 @@
+// gdn_states.hip -- C ABI of the operators on a pool of recurrent states
+// (declared in include/gdn.h): argument checks and launches on the caller's
+// stream.  No workspace, no allocation, no synchronisation.
+#include <hip/hip_runtime.h>
+
+#include "gdn.h"
+#include "gdn_host.h"
+#include "gdn_states.h"
+
+using namespace gdn;
+
+namespace {
+
+constexpr int kMaxNodes = 64;   // tree nodes per row: one per lane of a wave
+
+gdn_status validate_pool(const gdn_pool_shape *s, bool slots) {
+  if (!s) return GDN_ERR_NULL;
+  if (s->dtype != GDN_F32 && s->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (s->o_dtype != GDN_F32 && s->o_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (s->B < 1 || s->n < 1 || s->n > kMaxNodes || s->H_qk < 1 || s->H_v < 1 || s->H_v % s->H_qk) return GDN_ERR_SHAPE;
+  if (s->d_k != D || s->d_v != D || s->n_slots < 1 || (s->g_fixed & ~1)) return GDN_ERR_SHAPE;
+  if (!slots && s->n_slots < s->B) return GDN_ERR_SHAPE;
+  // (row, value head, column part) in a 1-D grid of at most 8 parts
+  if ((int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+
+StateArgs pool_args(const gdn_pool_shape &s) {
+  StateArgs a{};
+  a.B = s.B; a.n = s.n; a.Hqk = s.H_qk; a.Hv = s.H_v; a.n_slots = s.n_slots; a.g_fixed = s.g_fixed;
+  return a;
+}
+
+// Columns of a state per workgroup of the step and of the commit.
+int state_cols(const gdn_pool_shape &s) {
+  const int64_t units = (int64_t)s.B * s.H_v;
+  return units >= 512 ? 128 : units >= 128 ? 64 : 32;
+}
+
+template <typename F>
+gdn_status with_types(const gdn_pool_shape &s, F &&f) {
+  if (s.dtype == GDN_BF16)
+    return s.o_dtype == GDN_BF16 ? f(__bf16{}, __bf16{}) : f(__bf16{}, float{});
+  return s.o_dtype == GDN_BF16 ? f(float{}, __bf16{}) : f(float{}, float{});
+}
+
+template <int COLS, typename TI, typename TO>
+gdn_status launch_step(const StateArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL((step_kernel<COLS, TI, TO>), dim3((unsigned)((int64_t)a.B * a.Hv * (D / COLS))), dim3(256), 0, st, a);
+  return check_launch();
+}
+
+template <int COLS, typename TI>
+gdn_status launch_commit(const StateArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL((tree_commit_kernel<COLS, TI>), dim3((unsigned)((int64_t)a.B * a.Hv * (D / COLS))), dim3(256), 0, st, a);
+  return check_launch();
+}
+
+template <int MT, typename TI, typename TO, bool DELTA>
+gdn_status launch_tree(const StateArgs &a, hipStream_t st) {
+  const int64_t units = (int64_t)a.B * a.Hv;
+  if (units >= 512)
+    hipLaunchKernelGGL((tree_kernel<MT, 2, TI, TO, DELTA>), dim3((unsigned)units), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((tree_kernel<MT, 1, TI, TO, DELTA>), dim3((unsigned)(2 * units)), dim3(256), 0, st, a);
+  return check_launch();
+}
+
+template <typename TI, typename TO, bool DELTA>
+gdn_status run_tree(const StateArgs &a, hipStream_t st) {
+  if (a.n <= 16) return launch_tree<1, TI, TO, DELTA>(a, st);
+  if (a.n <= 32) return launch_tree<2, TI, TO, DELTA>(a, st);
+  return launch_tree<4, TI, TO, DELTA>(a, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_step(const gdn_pool_shape *s, const void *q, const void *k, const void *v, const float *g,
+                    const float *beta, const int32_t *slots, float *state, void *o, void *hip_stream) {
+  GDN_TRY(validate_pool(s, slots));
+  if (s->n != 1) return GDN_ERR_SHAPE;
+  if (!q || !k || !v || !g || !state || !o) return GDN_ERR_NULL;
+  for (const void *p : {q, k, v, (const void *)g, (const void *)beta, (const void *)slots, (const void *)state,
+                        (const void *)o})
+    if (misaligned(p)) return GDN_ERR_ALIGN;
+  StateArgs a = pool_args(*s);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.slots = slots; a.state = state; a.o = o;
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  return with_types(*s, [&](auto ti, auto to) -> gdn_status {
+    using TI = decltype(ti);
+    using TO = decltype(to);
+    switch (state_cols(*s)) {
+      case 128: return launch_step<128, TI, TO>(a, st);
+      case 64: return launch_step<64, TI, TO>(a, st);
+      default: return launch_step<32, TI, TO>(a, st);
+    }
+  });
+}
+
+gdn_status gdn_tree_fwd(const gdn_pool_shape *s, const void *q, const void *k, const void *v, const float *g,
+                        const float *beta, const int32_t *parents, const int32_t *slots, const float *state, void *o,
+                        float *u, void *hip_stream) {
+  GDN_TRY(validate_pool(s, slots));
+  if (!q || !k || !v || !g || !parents || !state || !o || !u) return GDN_ERR_NULL;
+  for (const void *p : {q, k, v, (const void *)g, (const void *)beta, (const void *)parents, (const void *)slots,
+                        (const void *)state, (const void *)o, (const void *)u})
+    if (misaligned(p)) return GDN_ERR_ALIGN;
+  StateArgs a = pool_args(*s);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.parents = parents; a.slots = slots;
+  a.state = const_cast<float *>(state); a.o = o; a.u = u;
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  return with_types(*s, [&](auto ti, auto to) -> gdn_status {
+    using TI = decltype(ti);
+    using TO = decltype(to);
+    return beta ? run_tree<TI, TO, true>(a, st) : run_tree<TI, TO, false>(a, st);
+  });
+}
+
+gdn_status gdn_tree_commit(const gdn_pool_shape *s, const void *k, const float *u, const float *g,
+                           const int32_t *parents, const int32_t *last, const int32_t *slots, float *state,
+                           void *hip_stream) {
+  GDN_TRY(validate_pool(s, slots));
+  if (!k || !u || !g || !parents || !last || !state) return GDN_ERR_NULL;
+  for (const void *p : {k, (const void *)u, (const void *)g, (const void *)parents, (const void *)last,
+                        (const void *)slots, (const void *)state})
+    if (misaligned(p)) return GDN_ERR_ALIGN;
+  StateArgs a = pool_args(*s);
+  a.k = k; a.u_in = u; a.g = g; a.parents = parents; a.last = last; a.slots = slots; a.state = state;
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  auto run = [&](auto ti) -> gdn_status {
+    using TI = decltype(ti);
+    switch (state_cols(*s)) {
+      case 128: return launch_commit<128, TI>(a, st);
+      case 64: return launch_commit<64, TI>(a, st);
+      default: return launch_commit<32, TI>(a, st);
+    }
+  };
+  return s->dtype == GDN_BF16 ? run(__bf16{}) : run(float{});
+}
+
+}  // extern "C"
