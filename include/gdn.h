@@ -413,6 +413,66 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const flo
                            const float *g, const int32_t *parents, const int32_t *last,
                            const int32_t *slots, float *state, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay per head, in chunks (prompts and training):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ * (the rule at the top of this file without the correction; gdn_step with
+ * beta = NULL is its single-token form).
+ *   B        batch rows (packed: sequences)
+ *   T        tokens per row (packed: in all)
+ *   H_qk, H_v, d_k, d_v, dtype, o_dtype   as in gdn_shape
+ *   g_fixed  0: log decays per token, g [B, T, H_v]; 1: one per value head,
+ *            g [H_v]
+ * Chunks and segments are the library's choice.  Limits: H_v <= 2^15,
+ * B * H_v <= 2^26, B * T < 2^31.  A log decay of -inf (a hard reset) is allowed. */
+typedef struct {
+  int32_t B, T, H_qk, H_v, d_k, d_v, g_fixed;
+  int32_t dtype, o_dtype;
+} gdn_linear_shape;
+
+/* Bytes of device workspace of gdn_linear_chunk_fwd (GDN_LINEAR_FWD),
+ * gdn_linear_chunk_fwd_varlen or gdn_linear_chunk_bwd (written to *bytes; 0
+ * where none is needed, ws may then be NULL).  It carries nothing between
+ * calls. */
+#define GDN_LINEAR_FWD 0
+#define GDN_LINEAR_VARLEN 1
+#define GDN_LINEAR_BWD 2
+gdn_status gdn_workspace_size_linear(const gdn_linear_shape *shape, int32_t kind, size_t *bytes);
+
+/* The forward.
+ *   q, k [B, T, H_qk, d_k], v [B, T, H_v, d_v] dtype; g fp32 as above;
+ *   h0 [B, H_v, d_k, d_v] fp32 initial state, NULL = zero
+ *   o [B, T, H_v, d_v] o_dtype (written); h_T [B, H_v, d_k, d_v] fp32 final
+ *   state, NULL = not wanted (written). */
+gdn_status gdn_linear_chunk_fwd(const gdn_linear_shape *shape, const void *q, const void *k,
+                                const void *v, const float *g, const float *h0, void *o,
+                                float *h_T, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* The forward over packed sequences: as gdn_chunk_fwd_varlen packs them
+ * (cu_seqlens [B + 1] int32 DEVICE array, a partition of [0, T]; planned on
+ * the device; for other offsets the results are unspecified, but nothing
+ * outside the tensors and the workspace is touched).  Each sequence has its
+ * own h0 and h_T [B, H_v, d_k, d_v]; an empty one's h_T is its h0. */
+gdn_status gdn_linear_chunk_fwd_varlen(const gdn_linear_shape *shape, const int32_t *cu_seqlens,
+                                       const void *q, const void *k, const void *v,
+                                       const float *g, const float *h0, void *o, float *h_T,
+                                       void *ws, size_t ws_bytes, void *hip_stream);
+
+/* The gradients of L = sum_t <o_t, dO_t> + <h_T, dh_T>.
+ *   dO [B, T, H_v, d_v] dtype (the inputs' type); dh_T [B, H_v, d_k, d_v]
+ *   fp32 or NULL (zero); h0 as given to the forward
+ *   dq, dk [B, T, H_qk, d_k] (the sum over the value heads that read a head),
+ *   dv [B, T, H_v, d_v] dtype, each rounded once from fp32; dg fp32, shaped
+ *   as g (fixed decays: the sum over all tokens); dh0 [B, H_v, d_k, d_v] fp32
+ *   or NULL.  shape->o_dtype is not used.
+ * dg is formed from differences <q_t, dq_t> - <k_t, dk_t>: its error is about
+ * 1e-6 of |q_t| |dq_t| + |k_t| |dk_t|, also where decays are so strong that dg
+ * itself is far smaller. */
+gdn_status gdn_linear_chunk_bwd(const gdn_linear_shape *shape, const void *q, const void *k,
+                                const void *v, const float *g, const float *h0, const void *dO,
+                                const float *dh_T, void *dq, void *dk, void *dv, float *dg,
+                                float *dh0, void *ws, size_t ws_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

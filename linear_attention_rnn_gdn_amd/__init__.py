@@ -12,6 +12,10 @@ Functions (same names as the C entry points, without the ``gdn_`` prefix):
   compose_prefix(A, Bm, h_init=None, split_bf16=False)          -> (h_in, h_final)
   chunk_transform(k, v, g, beta, chunk=128, want_T=False)       -> (G, T, W, U)
   workspace_size(...), validate(...)
+Linear attention with a decay per head (the rule without the correction):
+  linear_chunk_fwd(q, k, v, g, h0=None)                         -> (o, h_T)
+  linear_chunk_fwd_varlen(q, k, v, g, cu_seqlens, h0=None)      -> (o, h_T)
+  linear_chunk_bwd(q, k, v, g, dO, h0=None, dh_T=None)          -> gradients
 States in a pool [n_slots,H_v,d_k,d_v], for serving (beta=None: the linear rule):
   step(q, k, v, g, beta, state, slots=None)                     -> o
   tree_fwd(q, k, v, g, beta, parents, state, slots=None)        -> (o, u)
@@ -44,6 +48,11 @@ class GdnPoolShape(ctypes.Structure):
                 ("B", "n", "H_qk", "H_v", "d_k", "d_v", "n_slots", "g_fixed", "dtype", "o_dtype")]
 
 
+class GdnLinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "T", "H_qk", "H_v", "d_k", "d_v", "g_fixed", "dtype", "o_dtype")]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS.get(status, status)} (status {status})")
@@ -57,7 +66,8 @@ SYMBOLS = ("gdn_status_str", "gdn_validate", "gdn_workspace_size", "gdn_workspac
            "gdn_chunk_fwd_stages", "gdn_chunk_fwd_timed", "gdn_chunk_fold", "gdn_compose_prefix",
            "gdn_chunk_transform", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_affine",
            "gdn_workspace_size_bwd", "gdn_chunk_bwd_state", "gdn_workspace_size_bwd_grads", "gdn_chunk_bwd",
-           "gdn_step", "gdn_tree_fwd", "gdn_tree_commit")
+           "gdn_step", "gdn_tree_fwd", "gdn_tree_commit", "gdn_workspace_size_linear", "gdn_linear_chunk_fwd",
+           "gdn_linear_chunk_fwd_varlen", "gdn_linear_chunk_bwd")
 STAGE_PREP, STAGE_FOLD, STAGE_PREFIX, STAGE_WALK, STAGE_OUT, STAGE_ALL = 1, 2, 4, 8, 16, 31
 
 
@@ -112,6 +122,15 @@ def lib():
         L.gdn_tree_fwd.restype = I
         L.gdn_tree_commit.argtypes = [PP] + [P] * 8
         L.gdn_tree_commit.restype = I
+        LP = ctypes.POINTER(GdnLinearShape)
+        L.gdn_workspace_size_linear.argtypes = [LP, I, ctypes.POINTER(SZ)]
+        L.gdn_workspace_size_linear.restype = I
+        L.gdn_linear_chunk_fwd.argtypes = [LP] + [P] * 8 + [SZ, P]
+        L.gdn_linear_chunk_fwd.restype = I
+        L.gdn_linear_chunk_fwd_varlen.argtypes = [LP] + [P] * 9 + [SZ, P]
+        L.gdn_linear_chunk_fwd_varlen.restype = I
+        L.gdn_linear_chunk_bwd.argtypes = [LP] + [P] * 13 + [SZ, P]
+        L.gdn_linear_chunk_bwd.restype = I
         _lib = L
     return _lib
 
@@ -565,3 +584,124 @@ def tree_commit(k, u, g, parents, last, state, slots=None, stream=None):
         _check(lib().gdn_tree_commit(shape, _addr(k), _addr(u), _addr(g), _addr(parents), _addr(last), _addr(slots),
                                      _addr(state), st), "gdn_tree_commit")
     return state
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay per head, in chunks
+
+LINEAR_FWD, LINEAR_VARLEN, LINEAR_BWD = 0, 1, 2
+
+
+def workspace_size_linear(shape: GdnLinearShape, kind: int) -> int:
+    """Workspace bytes of linear_chunk_fwd (LINEAR_FWD), linear_chunk_fwd_varlen
+    (LINEAR_VARLEN; shape.B = sequences) or linear_chunk_bwd (LINEAR_BWD)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_workspace_size_linear(shape, kind, ctypes.byref(n)), "gdn_workspace_size_linear")
+    return int(n.value)
+
+
+def _linear_inputs(q, k, v, g):
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (g, "g")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must have 4 dimensions")
+    _dt(k.dtype)
+    B, T, Hqk, dk = k.shape
+    Hv, dv = v.shape[2:]
+    dev = k.device
+    fixed, gshape = _decay_shape(g, (B, T, Hv))
+    _check_tensors(dev, (q, "q", k.dtype, (B, T, Hqk, dk)), (k, "k", k.dtype, k.shape), (v, "v", k.dtype, (B, T, Hv, dv)),
+                   (g, "g", torch.float32, gshape))
+    return B, T, Hqk, Hv, dk, dv, fixed, dev
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _check_tensors(dev, (workspace, "workspace", torch.uint8, (workspace.numel(),)))
+    return workspace
+
+
+def _linear_fwd(rows, cu, q, k, v, g, h0, o_dtype, output_final_state, workspace, out, final_state, stream):
+    B, T, Hqk, Hv, dk, dv, fixed, dev = _linear_inputs(q, k, v, g)
+    n = B if rows is None else rows
+    state = (n, Hv, dk, dv)
+    if h0 is not None:
+        _check_tensors(dev, (h0, "h0", torch.float32, state))
+    if out is not None:
+        _check_tensors(dev, (out, "o", o_dtype, (B, T, Hv, dv)))
+    if final_state is not None:
+        _check_tensors(dev, (final_state, "h_T", torch.float32, state))
+    shape = GdnLinearShape(n, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), _dt(o_dtype))
+    need = workspace_size_linear(shape, LINEAR_FWD if rows is None else LINEAR_VARLEN)
+    with _On(dev, stream) as st:
+        ws = _workspace(workspace, need, dev)
+        o = out if out is not None else torch.empty((B, T, Hv, dv), dtype=o_dtype, device=dev)
+        hT = None
+        if output_final_state:
+            hT = final_state if final_state is not None else torch.empty(state, dtype=torch.float32, device=dev)
+        args = (_addr(q), _addr(k), _addr(v), _addr(g), _addr(h0), _addr(o), _addr(hT), _addr(ws), ws.numel(), st)
+        if rows is None:
+            _check(lib().gdn_linear_chunk_fwd(shape, *args), "gdn_linear_chunk_fwd")
+        else:
+            _check(lib().gdn_linear_chunk_fwd_varlen(shape, _addr(cu), *args), "gdn_linear_chunk_fwd_varlen")
+    return o, hT
+
+
+def linear_chunk_fwd(q, k, v, g, h0=None, o_dtype=torch.float32, output_final_state=True, workspace=None, out=None,
+                     final_state=None, stream=None):
+    """Linear attention with a decay per head (gdn_linear_chunk_fwd):
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k [B,T,H_qk,d_k]; v [B,T,H_v,d_v] (bf16 or fp32); g [B,T,H_v] fp32, or
+    [H_v] for decays that do not depend on the token; h0 [B,H_v,d_k,d_v] fp32
+    or None.  Returns (o [B,T,H_v,d_v] o_dtype, h_T or None)."""
+    return _linear_fwd(None, None, q, k, v, g, h0, o_dtype, output_final_state, workspace, out, final_state, stream)
+
+
+def linear_chunk_fwd_varlen(q, k, v, g, cu_seqlens, h0=None, o_dtype=torch.float32, output_final_state=True,
+                            workspace=None, out=None, final_state=None, stream=None):
+    """linear_chunk_fwd over packed sequences (gdn_linear_chunk_fwd_varlen):
+    the batch dimension of q, k, v (and g) is 1; cu_seqlens as in
+    chunk_fwd_varlen (n + 1 int32 offsets on the device, or a Python
+    sequence); h0 and h_T [n,H_v,d_k,d_v]."""
+    if isinstance(k, torch.Tensor) and k.dim() == 4 and k.shape[0] != 1:
+        raise ValueError("packed sequences: the batch dimension of q, k, v, g must be 1")
+    if not isinstance(cu_seqlens, torch.Tensor):
+        cu_seqlens = torch.tensor(list(cu_seqlens), dtype=torch.int32, device=k.device)
+    n = cu_seqlens.numel() - 1
+    if n < 1:
+        raise ValueError("cu_seqlens must hold at least two offsets")
+    _check_tensors(k.device, (cu_seqlens, "cu_seqlens", torch.int32, (n + 1,)))
+    return _linear_fwd(n, cu_seqlens, q, k, v, g, h0, o_dtype, output_final_state, workspace, out, final_state, stream)
+
+
+def linear_chunk_bwd(q, k, v, g, dO, h0=None, dh_T=None, workspace=None, out=None, stream=None):
+    """Gradients of sum_t <o_t, dO_t> + <h_T, dh_T> through linear_chunk_fwd
+    (gdn_linear_chunk_bwd).  dO [B,T,H_v,d_v] in the inputs' dtype; h0, dh_T
+    [B,H_v,d_k,d_v] fp32 or None.  Returns a dict (``out``: such a dict to
+    write into): dq, dk [B,T,H_qk,d_k], dv [B,T,H_v,d_v] in the inputs' dtype,
+    dg fp32 shaped as g, dh0 [B,H_v,d_k,d_v] fp32."""
+    B, T, Hqk, Hv, dk, dv, fixed, dev = _linear_inputs(q, k, v, g)
+    state = (B, Hv, dk, dv)
+    _check_tensors(dev, (dO, "dO", k.dtype, (B, T, Hv, dv)))
+    for name, x in (("h0", h0), ("dh_T", dh_T)):
+        if x is not None:
+            _check_tensors(dev, (x, name, torch.float32, state))
+    want = dict(dq=(k.dtype, (B, T, Hqk, dk)), dk=(k.dtype, (B, T, Hqk, dk)), dv=(k.dtype, (B, T, Hv, dv)),
+                dg=(torch.float32, tuple(g.shape)), dh0=(torch.float32, state))
+    if out is not None:
+        for name, (dt, sh) in want.items():
+            _check_tensors(dev, (out[name], name, dt, sh))
+    shape = GdnLinearShape(B, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), F32)
+    need = workspace_size_linear(shape, LINEAR_BWD)
+    with _On(dev, stream) as st:
+        ws = _workspace(workspace, need, dev)
+        if out is None:
+            out = {name: torch.empty(sh, dtype=dt, device=dev) for name, (dt, sh) in want.items()}
+        _check(lib().gdn_linear_chunk_bwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(h0), _addr(dO),
+                                          _addr(dh_T), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
+                                          _addr(out["dg"]), _addr(out["dh0"]), _addr(ws), ws.numel(), st),
+               "gdn_linear_chunk_bwd")
+    return out
