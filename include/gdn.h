@@ -423,7 +423,7 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const flo
  *   H_qk, H_v, d_k, d_v, dtype, o_dtype   as in gdn_shape
  *   g_fixed  0: log decays per token, g [B, T, H_v]; 1: one per value head,
  *            g [H_v]
- * Chunks and segments are the library's choice.  Limits: H_v <= 2^15,
+ * Chunks and segments are the library's choice.  Limits: H_v <= 2^14,
  * B * H_v <= 2^26, B * T < 2^31.  A log decay of -inf (a hard reset) is allowed. */
 typedef struct {
   int32_t B, T, H_qk, H_v, d_k, d_v, g_fixed;

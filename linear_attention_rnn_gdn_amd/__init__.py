@@ -24,6 +24,7 @@ States in a pool [n_slots,H_v,d_k,d_v], for serving (beta=None: the linear rule)
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -457,60 +458,89 @@ def chunk_transform(k, v, g, beta, chunk=128, want_T=False, stream=None):
 # states in a pool: the single-token step, drafted trees
 
 
+# The current stream's handle of a device, without building a Stream object
+# (a single-token step takes the GPU a few microseconds: so may its checks).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
-    """The stream a call goes to: ``stream``, or the current stream of the
-    tensors' device (which is made current for the launch).  Outputs and
-    workspace allocated inside belong to that stream."""
-    __slots__ = ("handle", "_stack")
+    """A call on a stream of the caller's, or on a device that is not the
+    current one (which is made current for the launch).  Outputs and workspace
+    allocated inside belong to that stream."""
+    __slots__ = ("dev", "ctx")
 
     def __init__(self, dev, stream):
-        self._stack = []
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-            self._stack.append(torch.cuda.stream(stream))
-        elif torch.cuda.current_device() != dev.index:
-            self._stack.append(torch.cuda.device(dev))
-        self.handle = stream
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+        self.dev = dev
+        self.ctx = torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        for c in self._stack:
-            c.__enter__()
-        return (torch.cuda.current_stream() if self.handle is None else self.handle).cuda_stream
+        self.ctx.__enter__()
+        return _raw_stream(self.dev.index)
 
     def __exit__(self, *exc):
-        for c in reversed(self._stack):
-            c.__exit__(*exc)
+        self.ctx.__exit__(*exc)
+
+
+class _Here:
+    """The current stream of the current device."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _on(dev, stream):
+    """Context of a launch: enters the stream the call goes to (``stream``, or
+    the current stream of the tensors' device) and gives its handle."""
+    index = dev.index
+    if stream is None and index == torch.cuda.current_device():
+        return _Here(_raw_stream(index))
+    return _On(dev, stream)
 
 
 def _check_tensors(dev, *items):
     """Each item: (tensor, name, dtype, shape); raises what _need raises."""
+    index = dev.index
     for t, name, dtype, shape in items:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.device == dev and t.is_cuda):
-            _need(t, name, dtype, shape, dev)
+        if not (type(t) is torch.Tensor and t.get_device() == index and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous()):
+            _need(t, name, dtype, shape, dev)   # (a subclass of Tensor that fits passes here)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
+def _pool_shape(*sizes):
+    return GdnPoolShape(*sizes)
+
+
 def _pool_dims(k, Hv_of, state, slots, lead):
-    """Sizes of a call on a pool: checks k and the pool; ``lead``: leading
-    dimensions before the heads (1: rows, 2: rows and nodes)."""
+    """Sizes of a call on a pool, and what is to be checked of k, the pool and
+    the slots; ``lead``: leading dimensions before the heads (1: rows, 2: rows
+    and nodes)."""
     if not isinstance(k, torch.Tensor) or not isinstance(Hv_of, torch.Tensor) or not isinstance(state, torch.Tensor):
         raise TypeError("k, v (u) and state must be tensors")
-    if k.dim() != lead + 2 or Hv_of.dim() != lead + 2 or state.dim() != 4:
+    ks, vs, ss = k.shape, Hv_of.shape, state.shape
+    if len(ks) != lead + 2 or len(vs) != lead + 2 or len(ss) != 4:
         raise ValueError(f"k and v (u) must have {lead + 2} dimensions and state 4")
-    _dt(k.dtype)
-    B, n = k.shape[0], (k.shape[1] if lead == 2 else 1)
-    Hqk, dk = k.shape[-2:]
-    Hv, dv = Hv_of.shape[-2:]
-    dev = k.device
-    _check_tensors(dev, (k, "k", k.dtype, k.shape), (state, "state", torch.float32, (state.shape[0], Hv, dk, dv)))
+    dt = k.dtype
+    _dt(dt)
+    Hv, dv, dk = vs[-2], vs[-1], ks[-1]
+    items = [(k, "k", dt, ks), (state, "state", torch.float32, (ss[0], Hv, dk, dv))]
     if slots is not None:
-        _check_tensors(dev, (slots, "slots", torch.int32, (B,)))
-    return B, n, Hqk, Hv, dk, dv, state.shape[0], dev
+        items.append((slots, "slots", torch.int32, ks[:1]))
+    return ks[0], (ks[1] if lead == 2 else 1), ks[-2], Hv, dk, dv, ss[0], k.device, items
 
 
 def _decay_shape(g, per_token):
@@ -526,15 +556,16 @@ def step(q, k, v, g, beta, state, slots=None, o_dtype=torch.float32, out=None, s
     device (None: row b has slot b).  A row whose slot is outside the pool,
     or is an earlier row's slot, gets a zero output and writes no state.
     Returns o [B,H_v,d_v] o_dtype."""
-    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, v, state, slots, 1)
+    B, n, Hqk, Hv, dk, dv, n_slots, dev, items = _pool_dims(k, v, state, slots, 1)
     fixed, gshape = _decay_shape(g, (B, Hv))
-    _check_tensors(dev, (q, "q", k.dtype, (B, Hqk, dk)), (v, "v", k.dtype, (B, Hv, dv)), (g, "g", torch.float32, gshape))
+    items += ((q, "q", k.dtype, (B, Hqk, dk)), (v, "v", k.dtype, (B, Hv, dv)), (g, "g", torch.float32, gshape))
     if beta is not None:
-        _check_tensors(dev, (beta, "beta", torch.float32, (B, Hv)))
+        items.append((beta, "beta", torch.float32, (B, Hv)))
     if out is not None:
-        _check_tensors(dev, (out, "o", o_dtype, (B, Hv, dv)))
-    shape = GdnPoolShape(B, 1, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
-    with _On(dev, stream) as st:
+        items.append((out, "o", o_dtype, (B, Hv, dv)))
+    _check_tensors(dev, *items)
+    shape = _pool_shape(B, 1, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
+    with _on(dev, stream) as st:
         o = out if out is not None else torch.empty((B, Hv, dv), dtype=o_dtype, device=dev)
         _check(lib().gdn_step(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(slots), _addr(state),
                               _addr(o), st), "gdn_step")
@@ -551,18 +582,19 @@ def tree_fwd(q, k, v, g, beta, parents, state, slots=None, o_dtype=torch.float32
     outputs); n <= 64; state [n_slots,H_v,d_k,d_v] fp32; slots as in step (rows
     may share a slot).  Returns (o [B,n,H_v,d_v] o_dtype, u [B,n,H_v,d_v] fp32,
     the values the nodes write, for tree_commit)."""
-    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, v, state, slots, 2)
+    B, n, Hqk, Hv, dk, dv, n_slots, dev, items = _pool_dims(k, v, state, slots, 2)
     fixed, gshape = _decay_shape(g, (B, n, Hv))
-    _check_tensors(dev, (q, "q", k.dtype, (B, n, Hqk, dk)), (v, "v", k.dtype, (B, n, Hv, dv)),
-                   (g, "g", torch.float32, gshape), (parents, "parents", torch.int32, (B, n)))
+    items += ((q, "q", k.dtype, (B, n, Hqk, dk)), (v, "v", k.dtype, (B, n, Hv, dv)),
+              (g, "g", torch.float32, gshape), (parents, "parents", torch.int32, (B, n)))
     if beta is not None:
-        _check_tensors(dev, (beta, "beta", torch.float32, (B, n, Hv)))
+        items.append((beta, "beta", torch.float32, (B, n, Hv)))
     if out is not None:
-        _check_tensors(dev, (out, "o", o_dtype, (B, n, Hv, dv)))
+        items.append((out, "o", o_dtype, (B, n, Hv, dv)))
     if values is not None:
-        _check_tensors(dev, (values, "u", torch.float32, (B, n, Hv, dv)))
-    shape = GdnPoolShape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
-    with _On(dev, stream) as st:
+        items.append((values, "u", torch.float32, (B, n, Hv, dv)))
+    _check_tensors(dev, *items)
+    shape = _pool_shape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
+    with _on(dev, stream) as st:
         o = out if out is not None else torch.empty((B, n, Hv, dv), dtype=o_dtype, device=dev)
         u = values if values is not None else torch.empty((B, n, Hv, dv), dtype=torch.float32, device=dev)
         _check(lib().gdn_tree_fwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(parents),
@@ -575,12 +607,12 @@ def tree_commit(k, u, g, parents, last, state, slots=None, stream=None):
     the state of node last[b], in place (last[b] outside the tree: left as it
     is).  k, g, parents as given to tree_fwd, u as returned by it; last [B]
     int32.  Rows naming one slot: the first is run.  Returns state."""
-    B, n, Hqk, Hv, dk, dv, n_slots, dev = _pool_dims(k, u, state, slots, 2)
+    B, n, Hqk, Hv, dk, dv, n_slots, dev, items = _pool_dims(k, u, state, slots, 2)
     fixed, gshape = _decay_shape(g, (B, n, Hv))
-    _check_tensors(dev, (u, "u", torch.float32, (B, n, Hv, dv)), (g, "g", torch.float32, gshape),
+    _check_tensors(dev, *items, (u, "u", torch.float32, (B, n, Hv, dv)), (g, "g", torch.float32, gshape),
                    (parents, "parents", torch.int32, (B, n)), (last, "last", torch.int32, (B,)))
-    shape = GdnPoolShape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), F32)
-    with _On(dev, stream) as st:
+    shape = _pool_shape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), F32)
+    with _on(dev, stream) as st:
         _check(lib().gdn_tree_commit(shape, _addr(k), _addr(u), _addr(g), _addr(parents), _addr(last), _addr(slots),
                                      _addr(state), st), "gdn_tree_commit")
     return state
@@ -590,6 +622,13 @@ def tree_commit(k, u, g, parents, last, state, slots=None, stream=None):
 # linear attention with a decay per head, in chunks
 
 LINEAR_FWD, LINEAR_VARLEN, LINEAR_BWD = 0, 1, 2
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_plan(kind, *sizes):
+    """(shape, workspace bytes) of a call's sizes."""
+    shape = GdnLinearShape(*sizes)
+    return shape, workspace_size_linear(shape, kind)
 
 
 def workspace_size_linear(shape: GdnLinearShape, kind: int) -> int:
@@ -633,9 +672,9 @@ def _linear_fwd(rows, cu, q, k, v, g, h0, o_dtype, output_final_state, workspace
         _check_tensors(dev, (out, "o", o_dtype, (B, T, Hv, dv)))
     if final_state is not None:
         _check_tensors(dev, (final_state, "h_T", torch.float32, state))
-    shape = GdnLinearShape(n, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), _dt(o_dtype))
-    need = workspace_size_linear(shape, LINEAR_FWD if rows is None else LINEAR_VARLEN)
-    with _On(dev, stream) as st:
+    shape, need = _linear_plan(LINEAR_FWD if rows is None else LINEAR_VARLEN, n, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype),
+                               _dt(o_dtype))
+    with _on(dev, stream) as st:
         ws = _workspace(workspace, need, dev)
         o = out if out is not None else torch.empty((B, T, Hv, dv), dtype=o_dtype, device=dev)
         hT = None
@@ -694,9 +733,8 @@ def linear_chunk_bwd(q, k, v, g, dO, h0=None, dh_T=None, workspace=None, out=Non
     if out is not None:
         for name, (dt, sh) in want.items():
             _check_tensors(dev, (out[name], name, dt, sh))
-    shape = GdnLinearShape(B, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), F32)
-    need = workspace_size_linear(shape, LINEAR_BWD)
-    with _On(dev, stream) as st:
+    shape, need = _linear_plan(LINEAR_BWD, B, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), F32)
+    with _on(dev, stream) as st:
         ws = _workspace(workspace, need, dev)
         if out is None:
             out = {name: torch.empty(sh, dtype=dt, device=dev) for name, (dt, sh) in want.items()}

@@ -146,6 +146,37 @@ __device__ __forceinline__ f32x4 quad_transpose(f32x4 v, int lane) {
   return v;
 }
 
+// Inclusive prefix sum over the wave's lanes by lane permutations of the
+// vector ALU (a shuffle through LDS per step would take longer than the rest
+// of a chunk's decays), and the value of one lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const long long v = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (long long)((unsigned long long)(unsigned)hi << 32 | (unsigned)lo));
+}
+__device__ __forceinline__ double wave_prefix(double x) {
+  x += dpp_or_zero<0x111, 0xf>(x);   // row_shr:1 .. 8 within 16 lanes
+  x += dpp_or_zero<0x112, 0xf>(x);
+  x += dpp_or_zero<0x114, 0xf>(x);
+  x += dpp_or_zero<0x118, 0xf>(x);
+  x += dpp_or_zero<0x142, 0xa>(x);   // row_bcast:15 into rows 1 and 3
+  x += dpp_or_zero<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double lane_value(double x, int l) {
+  const long long v = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_readlane((int)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
+  return __builtin_bit_cast(double, (long long)((unsigned long long)(unsigned)hi << 32 | (unsigned)lo));
+}
+
+__device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+__device__ __forceinline__ f32x4 load4(const __bf16 *p) {
+  const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+  return __builtin_bit_cast(f32x4, u32x4{w[0] << 16, w[0] & 0xffff0000u, w[1] << 16, w[1] & 0xffff0000u});
+}
+
 // How a walk is laid out for inputs of type TI: C tokens per chunk and planes
 // per input value.  fp32 inputs: three bf16 planes hold every bit, so all
 // products run on the bf16 matrix cores (6 of their passes against the 16
@@ -153,39 +184,68 @@ __device__ __forceinline__ f32x4 quad_transpose(f32x4 v, int lane) {
 template <typename TI> struct LinTile { static constexpr int C = 64, NPI = 1; };
 template <> struct LinTile<float> { static constexpr int C = 32, NPI = 3; };
 
-// Four waves; wave w holds columns 16 NTW w + .. of the state, all 128 rows:
-// result tile (m, t) has rows 16 m + 4 g + i and the columns
-//   dv(lr, t) = 4 NTW (lr / 4) + 4 t + lr % 4,
-// so that the wave's NTW tiles give a lane 4 NTW consecutive columns of a
-// transposed output tile, and four lanes the four elements of one transposing
-// LDS read.
+// NW waves; wave w holds 16 columns of the state, all 128 rows, in eight
+// result tiles.  Tile m's row 4 g + i is the state's row
+//   32 (m / 2) + 8 g + 4 (m % 2) + i,
+// so that a pair of tiles gives lane group g 8 consecutive rows: the pair is
+// the operand of the product with A's rows as these lie in memory.
 //
 // Per chunk: every wave multiplies its state (split into NPO planes) with all
 // rows of A (outputs transposed: state as the left operand, straight from its
-// result registers); wave w forms the 16-row strip w of the masked scores and
-// leaves them in LDS as NPO planes; after a barrier all waves add scores x C
+// result registers); the masked scores' 16 x 16 tiles are dealt out to the
+// waves, which leave them in LDS as NPO planes; after a barrier all waves add scores x C
 // for their columns, write their outputs, and add B^T (weighted C) to the
 // state (weighted C in three planes, so that the state keeps fp32 precision).
 // The chunk's operands sit in LDS in row-major order; products over tokens
 // read them with the transposing LDS read.  The next chunk's operands are
 // loaded into registers while this one is computed.
-template <int KIND_FOLD, int NTW, int NPO, typename TI, typename TO>
-__global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
-  constexpr bool FOLD = KIND_FOLD;
+// fn(i, j) for every pair of planes that mma_planes multiplies, in its order
+template <int NA, int NB, typename F>
+__device__ __forceinline__ void each_plane_pair(F &&fn) {
+  constexpr int M = NA > NB ? NA : NB;
+  auto at = [&](auto s, auto i) __attribute__((always_inline)) {
+    if constexpr (i.value < NA && s.value >= i.value && s.value - i.value < NB)
+      fn(i, std::integral_constant<int, s.value - i.value>{});
+  };
+  auto sum = [&](auto s) __attribute__((always_inline)) {
+    at(s, std::integral_constant<int, 0>{});
+    at(s, std::integral_constant<int, 1>{});
+    at(s, std::integral_constant<int, 2>{});
+  };
+  if constexpr (M > 2) sum(std::integral_constant<int, 2>{});
+  if constexpr (M > 1) sum(std::integral_constant<int, 1>{});
+  sum(std::integral_constant<int, 0>{});
+}
+template <int N, typename F>
+__device__ __forceinline__ float sum_of(F &&x) {
+  float s = x(0);
+#pragma unroll
+  for (int i = 1; i < N; ++i) s += x(i);
+  return s;
+}
+
+enum : int { LIN_FWD = 0, LIN_FOLD = 1, LIN_GRAD = 2 };
+// waves per SIMD that the registers are shared out for: two workgroups per
+// compute unit (one for fp32 inputs, whose planes fill more than half the LDS)
+template <typename TI, int NW> constexpr int lin_waves() { return std::is_same<TI, float>::value ? NW / 4 : NW / 2; }
+template <int KIND, int NW, int NPO, typename TI, typename TO>
+__global__ __launch_bounds__(64 * NW, (lin_waves<TI, NW>())) void linear_kernel(LinArgs p) {
+  constexpr bool FOLD = KIND == LIN_FOLD, GRAD = KIND == LIN_GRAD;
   using L = LinTile<TI>;
   constexpr int C = L::C, NPI = L::NPI, NR = C / 16, KB = C / 32;
-  constexpr int PA = D + 8, PB = D + 16, PP = C + 8;    // row pitches in LDS (elements)
-  constexpr int COLS = 64 * NTW;                        // state columns per workgroup
-  constexpr int PER = 16 / sizeof(TI), PIECES = D / PER, ROWS = 256 / PIECES, LD = C / ROWS;   // staging loads
-  __shared__ __attribute__((aligned(16))) __bf16 al[FOLD ? 1 : NPI][FOLD ? 8 : C * PA];
-  __shared__ __attribute__((aligned(16))) __bf16 bl[NPI][C * PB], cl[NPI][C * PB];
-  __shared__ __attribute__((aligned(16))) __bf16 pl[FOLD ? 1 : NPO][FOLD ? 8 : C * PP];
-  __shared__ double Fl[2][C];
+  constexpr int NTHR = 64 * NW;
+  constexpr int COLS = 16 * NW;                   // state columns per workgroup
+  constexpr int PER = 16 / sizeof(TI), PIECES = D / PER, ROWS = NTHR / PIECES, LD = C / ROWS;   // staging loads
+  // operands, rows of 128 in 16-byte pieces; see piece_of()
+  __shared__ __attribute__((aligned(256))) __bf16 al[FOLD ? 1 : NPI][FOLD ? 128 : C * D];
+  __shared__ __attribute__((aligned(256))) __bf16 bl[NPI][C * D], cl[NPI][C * D];
+  __shared__ __attribute__((aligned(256))) __bf16 pl[FOLD ? 1 : NPO][FOLD ? 128 : C * C];
+  __shared__ __attribute__((aligned(16))) double Fl[2][C];
   __shared__ __attribute__((aligned(16))) float fs[2][C], te[2][C];   // e^F, e^{F_end - F}
   __shared__ float fe[2];                                             // e^{F_end}
-  __shared__ float dots[FOLD ? 1 : 4][FOLD ? 1 : C];
-  __shared__ float crs[4];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, lr = lane & 15, g = lane >> 4;
+  __shared__ float dots[GRAD ? NW : 1][GRAD ? C : 1];
+  __shared__ float crs[NW];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, lr = lane & 15, g = lane >> 4;
 
   int unit, part;
   const int R = p.Hv / p.Hqk;
@@ -199,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
   GDN_PICK(init); GDN_PICK(seg); GDN_PICK(fin); GDN_PICK(dec); GDN_PICK(out); GDN_PICK(out_f32);
   GDN_PICK(x); GDN_PICK(gx); GDN_PICK(dot); GDN_PICK(xs); GDN_PICK(xs_last); GDN_PICK(cross);
 #undef GDN_PICK
-  const int col0 = (part % (D / COLS)) * COLS + 16 * NTW * wave;   // this wave's first column
+  const int col0 = (part % (D / COLS)) * COLS + 16 * wave;   // this wave's first column
   const Seg sg = segment(p, sidx);
   if (sg.rows < 0) return;
   const bool enters = ro.rev ? sg.last : sg.first, leaves = ro.rev ? sg.first : sg.last;
@@ -207,11 +267,9 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
   const int nch = (sg.rows + C - 1) / C;
   const size_t sth = ((size_t)sidx * p.Hv + hv) * (D * D), sqh = ((size_t)sg.seq * p.Hv + hv) * (D * D);
 
-  f32x4 H[8][NTW];
+  f32x4 H[8];
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int t = 0; t < NTW; ++t) H[m][t] = zero4();
+  for (int m = 0; m < 8; ++m) H[m] = zero4();
   // this lane's place in a stored state, from a lane index the compiler cannot
   // see through: else it keeps the addresses alive from the first use to the last
   struct Place { int row, col; };
@@ -219,31 +277,33 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
     int l = lane;
     asm volatile("" : "+v"(l));
     const int q = l & 15;
-    const int along = 4 * (l >> 4), c = col0 + 4 * NTW * (q >> 2);
+    const int along = 8 * (l >> 4), c = col0 + 4 * (q >> 2);
     return ro.trans ? Place{along, c + (q & 3)} : Place{along + (q & 3), c};
   };
-  // state element (row 16 m + 4 g + i, column dv): read along whichever of the two is contiguous
-  auto load_state = [&](const float *S, auto &&put) __attribute__((always_inline)) {
+  // state element (row state_row(m, g, i), column): read along whichever of the two is contiguous
+  // (all loads first, then one branch around the transpositions: a branch per
+  // tile would wait for each load by itself)
+  auto load_state = [&](const float *S, f32x4 (&x)[8]) __attribute__((always_inline)) {
     const Place pl = state_place();
     const unsigned at = ro.trans ? pl.col * D + pl.row : pl.row * D + pl.col;
+    const unsigned dm = ro.trans ? 4 : 4 * D;   // rows: 32 (m / 2) + 4 (m % 2)
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
+    for (int m = 0; m < 8; ++m) x[m] = *reinterpret_cast<const f32x4 *>(S + (at + (8 * (m >> 1) + (m & 1)) * dm));
+    if (!ro.trans) {
 #pragma unroll
-      for (int t = 0; t < NTW; ++t) {
-        const unsigned d = ro.trans ? 4 * t * D + 16 * m : 16 * m * D + 4 * t;
-        f32x4 x = *reinterpret_cast<const f32x4 *>(S + (at + d));
-        if (!ro.trans) x = quad_transpose(x, lane);
-        put(m, t, x);
-      }
+      for (int m = 0; m < 8; ++m) x[m] = quad_transpose(x[m], lane);
+    }
   };
-  if (!FOLD) {
-    const float *S = enters ? (ro.init ? ro.init + sqh : nullptr) : ro.seg + sth;
-    if (S) load_state(S, [&](int m, int t, const f32x4 &x) { H[m][t] = x; });
-  }
-
   // token of row r of chunk n, in the order of the walk; staging loads
   auto token = [&](int at) __attribute__((always_inline)) { return ro.rev ? sg.start + sg.rows - 1 - at : sg.start + at; };
-  const int srow = tid / PIECES, scol = (tid % PIECES) * PER;
+  const int scol = (tid % PIECES) * PER;
+  // (opaque at each use: what is derived from it is cheap to form, and would
+  // fill registers if kept over the whole loop)
+  auto staging_row = [&]() __attribute__((always_inline)) -> int {
+    int r = tid / PIECES;
+    asm volatile("" : "+v"(r));
+    return r;
+  };
   // bytes between tokens; a chunk's first token in memory is uniform, so that
   // a lane's address is a scalar base and a 32-bit offset
   const int na = (p.Hv / ro.ga) * D * (int)sizeof(TI), nb = (p.Hv / ro.gb) * D * (int)sizeof(TI),
@@ -254,38 +314,55 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
   auto chunk_base = [&](int n) __attribute__((always_inline)) { return token(ro.rev ? min(n * C + C, sg.rows) - 1 : n * C); };
   u32x4 xa[FOLD ? 1 : LD], xb[LD], xc[LD];
   // (past the segment's end its last row is read, without a branch, and dropped on the way into LDS)
+  // token of row r of chunk n, from the chunk's base; rows past the end: the last row
+  auto row_token = [&](int n, int r) __attribute__((always_inline)) -> unsigned {
+    const int last = min(C, sg.rows - n * C) - 1, d = min(r, last);
+    return ro.rev ? last - d : d;
+  };
   auto load_chunk = [&](int n) __attribute__((always_inline)) {
+    const int srow = staging_row();
     const int lo = chunk_base(n);
     const char *qa = pa + (size_t)lo * na, *qb = pb + (size_t)lo * nb, *qc = pc + (size_t)lo * nc;
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const unsigned d = token(min(n * C + srow + i * ROWS, sg.rows - 1)) - lo, sb = scol * sizeof(TI);
-      if constexpr (!FOLD) xa[i] = *reinterpret_cast<const u32x4 *>(qa + (d * na + sb));
-      xb[i] = *reinterpret_cast<const u32x4 *>(qb + (d * nb + sb));
-      xc[i] = *reinterpret_cast<const u32x4 *>(qc + (d * nc + sb));
+      const unsigned d = row_token(n, srow + i * ROWS), sb = scol * sizeof(TI);
+      if constexpr (!FOLD) xa[i] = *reinterpret_cast<const u32x4 *>(qa + (__umul24(d, na) + sb));
+      xb[i] = *reinterpret_cast<const u32x4 *>(qb + (__umul24(d, nb) + sb));
+      xc[i] = *reinterpret_cast<const u32x4 *>(qc + (__umul24(d, nc) + sb));
     }
   };
-  auto put_piece = [&](auto &dst, int pitch, int row, const u32x4 &x) __attribute__((always_inline)) {
+  // Where piece c of row r lies: its index is XORed with the row's, the row's
+  // two low bits above its next two.  16 consecutive rows' pieces of one index
+  // are then in 16 different places (row reads), and so are 4 aligned pieces of
+  // 4 aligned rows (transposing reads): no bank conflicts in either.
+  auto piece_of = [&](int r, int c) __attribute__((always_inline)) -> int {
+    return r * D + ((c ^ ((r & 3) << 2 | (r >> 2 & 3))) << 3);
+  };
+  auto put_piece = [&](auto &dst, int row, const u32x4 &x) __attribute__((always_inline)) {
+    const int c = tid % PIECES;
     if constexpr (NPI == 1) {
-      *reinterpret_cast<u32x4 *>(&dst[0][row * pitch + scol]) = x;
+      *reinterpret_cast<u32x4 *>(&dst[0][piece_of(row, c)]) = x;
     } else {
+      const int at = piece_of(row, c >> 1) + 4 * (c & 1);
       unsigned w0[3], w1[3];
       const f32x4 y = __builtin_bit_cast(f32x4, x);
       split_pair<3>(y[0], y[1], w0);
       split_pair<3>(y[2], y[3], w1);
 #pragma unroll
-      for (int k = 0; k < NPI; ++k) *reinterpret_cast<u32x2 *>(&dst[k][row * pitch + scol]) = u32x2{w0[k], w1[k]};
+      for (int k = 0; k < NPI; ++k) *reinterpret_cast<u32x2 *>(&dst[k][at]) = u32x2{w0[k], w1[k]};
     }
   };
   auto store_chunk = [&](int n) __attribute__((always_inline)) {
+    const int srow = staging_row();
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       const int row = srow + i * ROWS;
       const bool on = n * C + row < sg.rows;
       const u32x4 z{0, 0, 0, 0};
-      if constexpr (!FOLD) put_piece(al, PA, row, on ? xa[i] : z);
-      put_piece(bl, PB, row, on ? xb[i] : z);
-      put_piece(cl, PB, row, on ? xc[i] : z);
+      // (A's and B's rows past the end meet zero rows of C, or give rows of the output that are not written)
+      if constexpr (!FOLD) put_piece(al, row, xa[i]);
+      put_piece(bl, row, xb[i]);
+      put_piece(cl, row, on ? xc[i] : z);
     }
   };
   // decays of chunk n: this lane's token's log decay, and (wave 0) the sums
@@ -297,13 +374,9 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
   double total = 0.;
   auto put_decay = [&](int buf, float gv) __attribute__((always_inline)) {
     const double own = log2_decay(gv);
-    double F = own;
-#pragma unroll
-    for (int d = 1; d < C; d <<= 1) {
-      const double y = __shfl_up(F, d);
-      if (lane >= d) F += y;
-    }
-    const double end = __shfl(F, C - 1);
+    const double F0 = wave_prefix(own);
+    const double end = lane_value(F0, C - 1);   // (lanes past the chunk add zero)
+    double F = F0;
     total += end;
     if (ro.rev) F -= own;
     if (lane < C) {
@@ -314,124 +387,142 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
     if (lane == 0) fe[buf] = decay_between(end, 0.);
   };
 
-  // LDS addresses as such (not generic pointers), so that a read's constant
-  // part goes into its offset field and all reads share one address register
+  // LDS addresses as such (not generic pointers), in bytes: what does not
+  // depend on the lane goes into a read's offset field
   typedef const __attribute__((address_space(3))) __bf16 *LdsB;
-  typedef __attribute__((address_space(3))) s16x4 *LdsT;
-  const LdsB tr_b = (LdsB)&bl[0][0] + (8 * g + (lr >> 2)) * PB + 4 * (lr & 3);
-  const LdsB tr_c = (LdsB)&cl[0][0] + (8 * g + (lr >> 2)) * PB + col0 + 4 * NTW * (lr & 3);
-  const LdsB row_a = (LdsB)&al[0][0] + lr * PA + 4 * g, row_b = (LdsB)&bl[0][0] + lr * PB + 4 * g;
-  const LdsB row_p = (LdsB)&pl[0][0] + lr * PP + 8 * g;
-  // 8 tokens x one column of an operand, transposed: tokens 32 kb + 8 g .., column `col` + the lane's
-  auto read_tr = [&](LdsB base, int k, int kb, int col) __attribute__((always_inline)) -> bf16x8 {
-    const LdsB q = base + k * (C * PB) + 32 * kb * PB + col;
+  auto lds = [](const __bf16 *q) __attribute__((always_inline)) -> unsigned { return (unsigned)(size_t)(LdsB)q; };
+  // 8 tokens (32 kb + 8 g ..) x one column, transposed: two reads of 4 tokens,
+  // h = 0, 1, at a lane's address ^ (16 h) + 4 rows
+  const int tr_row = 8 * g + (lr >> 2), tq = lr & 3;
+  unsigned tr_b = 2 * piece_of(tr_row, tq), tr_c0 = 2 * (piece_of(tr_row, (col0 >> 3) + (tq >> 1)) + 4 * (tq & 1));
+  auto read_tr = [&](unsigned base, unsigned at, int kb) __attribute__((always_inline)) -> bf16x8 {
+    typedef __attribute__((address_space(3))) s16x4 *LdsT;
     union { s16x4 h[2]; bf16x8 v; } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsT)q);
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsT)(q + 4 * PB));
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsT)(size_t)(at + (base + 64 * D * kb)));
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsT)(size_t)((at ^ 16) + (base + 64 * D * kb + 8 * D)));
     return u.v;
   };
-  // row lr of strip r, k order of two stacked result tiles: 32 kb + 4 g + {0..3}, 32 kb + 16 + 4 g + {0..3}
-  auto read_row = [&](LdsB base, int plane, int pitch, int r, int kb) __attribute__((always_inline)) -> bf16x8 {
-    typedef const __attribute__((address_space(3))) u32x2 *P2;
-    const LdsB q = base + plane + 16 * r * pitch + 32 * kb;
-    union { u32x2 h[2]; bf16x8 v; } u;
-    u.h[0] = *(P2)q;
-    u.h[1] = *(P2)(q + 16);
-    return u.v;
+  // B's columns of tile m (piece q of its 32-column block, the half by m's parity); C's, of the wave's tile
+  auto read_b = [&](int k, int kb, int m) __attribute__((always_inline)) -> bf16x8 {
+    return read_tr(lds(bl[k]) + 8 * (m & 1), tr_b ^ (64 * (m >> 1)), kb);
+  };
+  auto read_c = [&](int k, int kb) __attribute__((always_inline)) -> bf16x8 { return read_tr(lds(cl[k]), tr_c0, kb); };
+  // row lr of strip r of A or B, columns 32 kb + 8 g ..
+  unsigned row0 = 2 * piece_of(lr, g);
+  auto read_row = [&](const __bf16 *base, int r, int kb) __attribute__((always_inline)) -> bf16x8 {
+    return *(const __attribute__((address_space(3))) bf16x8 *)(size_t)((row0 ^ (64 * kb)) + (lds(base) + 32 * D * r));
   };
 
+  if (nch > 0) load_chunk(0);
+  if (!FOLD) {
+    const float *S = enters ? (ro.init ? ro.init + sqh : nullptr) : ro.seg + sth;
+    if (S) load_state(S, H);
+  }
+
+  // element (r, i) of the scores in LDS: rows of C, their 16-byte pieces
+  // permuted by the row so that 16 rows' pieces lie in different banks
+  auto score_at = [&](int r, int i) __attribute__((always_inline)) -> int {
+    return r * C + (((i >> 3) ^ (r & (C / 8 - 1))) << 3) + (i & 7);
+  };
+  unsigned row_p = 2 * score_at(lr, 8 * g);   // row lr of a strip of scores, columns 8 g ..
   if (nch > 0) {
-    load_chunk(0);
-    if (wave == 0) put_decay(0, load_decay(0));
+    if (wave == NW - 1) put_decay(0, load_decay(0));
     // scores of the 16 x 16 tiles above the diagonal that a 32-token block of C reads: zero, once
     if constexpr (!FOLD) {
-      for (int i = tid; i < NPO * (NR / 2) * 16 * 16; i += 256) {
-        const int k = i / (NR / 2 * 256), e = i % (NR / 2 * 256), q = e / 256, r = e / 16 % 16, c = e % 16;
-        pl[k][(32 * q + r) * PP + 32 * q + 16 + c] = (__bf16)0.f;
+      for (int i = tid; i < NPO * (NR / 2) * 16 * 4; i += NTHR) {
+        const int k = i / (NR / 2 * 64), e = i % (NR / 2 * 64), q = e / 64, r = e / 4 % 16, c = e % 4;
+        *reinterpret_cast<u32x2 *>(&pl[k][score_at(32 * q + r, 32 * q + 16 + 4 * c)]) = u32x2{0, 0};
       }
     }
     store_chunk(0);
   }
-  float gnext = nch > 1 && wave == 0 ? load_decay(1) : 0.f;
+  float gnext = nch > 1 && wave == NW - 1 ? load_decay(1) : 0.f;
   __syncthreads();
 
   for (int n = 0; n < nch; ++n) {
     const int buf = n & 1;
-    if (n + 1 < nch) load_chunk(n + 1);
-    f32x4 O[FOLD ? 1 : NTW][FOLD ? 1 : NR];
+    // (per chunk anew: the addresses derived from these are one XOR each, and
+    // would fill registers if kept over the whole loop)
+    asm volatile("" : "+v"(row0), "+v"(tr_b), "+v"(tr_c0), "+v"(row_p));
+    f32x4 O[FOLD ? 1 : NR];
     if constexpr (!FOLD) {
-      // masked scores, strip `wave` of rows (fewer strips than waves at C = 32)
-      if (wave < NR) {
-        bf16x8 fa[4][NPI];
+      // masked scores: the tiles on and below the diagonal dealt out to the waves
+      constexpr int TILES = NR * (NR + 1) / 2;
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
+      for (int i0 = 0; i0 < TILES; i0 += NW) {
+        const int ti = i0 + wave;
+        if (ti >= TILES) break;
+        const int mr = ti < 1 ? 0 : ti < 3 ? 1 : ti < 6 ? 2 : 3, mi = ti - mr * (mr + 1) / 2;
+        f32x4 s = zero4();
 #pragma unroll
-          for (int k = 0; k < NPI; ++k) fa[kb][k] = read_row(row_a, k * (C * PA), PA, wave, kb);
-        const double Fr = Fl[buf][16 * wave + lr];
-        for (int mi = 0; mi <= wave; ++mi) {
-          f32x4 s = zero4();
+        for (int kb = 0; kb < 4; ++kb) {
+          bf16x8 fa[NPI], fb[NPI];
 #pragma unroll
-          for (int kb = 0; kb < 4; ++kb) {
-            bf16x8 fb[NPI];
-#pragma unroll
-            for (int k = 0; k < NPI; ++k) fb[k] = read_row(row_b, k * (C * PB), PB, mi, kb);
-            mma_planes<NPI, NPI>(s, fb, fa[kb]);
+          for (int k = 0; k < NPI; ++k) {
+            fa[k] = read_row(al[k], mr, kb);
+            fb[k] = read_row(bl[k], mi, kb);
           }
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ci = 16 * mi + 4 * g + i;
-            x[i] = ci <= 16 * wave + lr ? s[i] * decay_between(Fr, Fl[buf][ci]) : 0.f;
-          }
-          unsigned w0[NPO], w1[NPO];
-          split_pair<NPO>(x[0], x[1], w0);
-          split_pair<NPO>(x[2], x[3], w1);
-#pragma unroll
-          for (int k = 0; k < NPO; ++k)
-            *reinterpret_cast<u32x2 *>(&pl[k][(16 * wave + lr) * PP + 16 * mi + 4 * g]) = u32x2{w0[k], w1[k]};
+          mma_planes<NPI, NPI>(s, fb, fa);
         }
+        float x[4];
+        const double Fr = Fl[buf][16 * mr + lr];
+        double Fi[4];   // (read before the mask, so that it is a select and no branch)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Fi[i] = Fl[buf][16 * mi + 4 * g + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = s[i] * decay_between(Fr, Fi[i]);
+          x[i] = 16 * mi + 4 * g + i <= 16 * mr + lr ? y : 0.f;
+        }
+        unsigned w0[NPO], w1[NPO];
+        split_pair<NPO>(x[0], x[1], w0);
+        split_pair<NPO>(x[2], x[3], w1);
+        const int at = score_at(16 * mr + lr, 16 * mi + 4 * g);
+#pragma unroll
+        for (int k = 0; k < NPO; ++k) *reinterpret_cast<u32x2 *>(&pl[k][at]) = u32x2{w0[k], w1[k]};
       }
-      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the next chunk's operands (the last chunk's again behind it: a load under
+    // a condition would keep the registers alive all around the loop)
+    __builtin_amdgcn_sched_barrier(0);
+    load_chunk(min(n + 1, nch - 1));
+    if constexpr (!FOLD) {
       // state x A, per token scaled by e^F
 #pragma unroll
-      for (int t = 0; t < NTW; ++t)
-#pragma unroll
-        for (int r = 0; r < NR; ++r) O[t][r] = zero4();
+      for (int r = 0; r < NR; ++r) O[r] = zero4();
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        bf16x8 h[NTW][NPO];
+        bf16x8 h[NPO];
+        float x[8];
 #pragma unroll
-        for (int t = 0; t < NTW; ++t) {
-          float x[8];
+        for (int j = 0; j < 8; ++j) x[j] = H[2 * kb + j / 4][j % 4];
+        split8<NPO>(x, h);
+        // two strips of rows at a time: products into the same tile stand apart
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = H[2 * kb + j / 4][t][j % 4];
-          split8<NPO>(x, h[t]);
+        for (int r = 0; r < NR; r += 2) {
+          bf16x8 f[2][NPI];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < NPI; ++k) f[j][k] = read_row(al[k], r + j, kb);
+          each_plane_pair<NPO, NPI>([&](auto ka, auto kb_) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              O[r + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h[ka], f[j][kb_], O[r + j], 0, 0, 0);
+          });
+          if (r) __builtin_amdgcn_sched_barrier(0);
         }
-        bf16x8 f[2][NPI];
-#pragma unroll
-        for (int k = 0; k < NPI; ++k) f[0][k] = read_row(row_a, k * (C * PA), PA, 0, kb);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          if (r + 1 < NR)
-#pragma unroll
-            for (int k = 0; k < NPI; ++k) f[(r + 1) & 1][k] = read_row(row_a, k * (C * PA), PA, r + 1, kb);
-#pragma unroll
-          for (int t = 0; t < NTW; ++t) mma_planes<NPO, NPI>(O[t][r], h[t], f[r & 1]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float e = fs[buf][16 * r + lr];
 #pragma unroll
-        for (int t = 0; t < NTW; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) O[t][r][i] *= e;
+        for (int i = 0; i < 4; ++i) O[r][i] *= e;
       }
     }
     __builtin_amdgcn_sched_barrier(0);   // (phases kept apart: operands of one only are live)
     // the next chunk's decays, while the scores settle
-    if (wave == 0 && n + 1 < nch) {
+    if (wave == NW - 1 && n + 1 < nch) {
       put_decay(buf ^ 1, gnext);
       if (n + 2 < nch) gnext = load_decay(n + 2);
     }
@@ -440,106 +531,109 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
       // scores x C
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        bf16x8 cf[NTW][NPI];
+        bf16x8 cf[NPI];
 #pragma unroll
-        for (int t = 0; t < NTW; ++t)
-#pragma unroll
-          for (int k = 0; k < NPI; ++k) cf[t][k] = read_tr(tr_c, k, kb, 4 * t);
+        for (int k = 0; k < NPI; ++k) cf[k] = read_c(k, kb);
 #pragma unroll
         for (int r = 2 * kb; r < NR; ++r) {
           bf16x8 ps[NPO];
 #pragma unroll
           for (int k = 0; k < NPO; ++k)
-            ps[k] = *(const __attribute__((address_space(3))) bf16x8 *)(row_p + k * (C * PP) + 16 * r * PP + 32 * kb);
-#pragma unroll
-          for (int t = 0; t < NTW; ++t) mma_planes<NPI, NPO>(O[t][r], cf[t], ps);
+            ps[k] = *(const __attribute__((address_space(3))) bf16x8 *)(size_t)((row_p ^ (64 * kb)) + (lds(pl[k]) + 32 * C * r));
+          mma_planes<NPI, NPO>(O[r], cf, ps);
+          if (r & 1) __builtin_amdgcn_sched_barrier(0);
         }
       }
-      // outputs: lane -> token 16 r + lr, columns 4 NTW g .. of the wave's
+      // outputs: lane -> token 16 r + lr, columns 4 g .. of the wave's
+      // (scalar base of the chunk, 32-bit offsets)
+      const int lo = chunk_base(n), oc = col0 + 4 * g;
+      auto row_of = [&](int r) __attribute__((always_inline)) -> unsigned { return row_token(n, 16 * r + lr); };
+      if (std::is_same<TO, float>::value || (GRAD && ro.out_f32)) {
+        char *o = static_cast<char *>(ro.out) + ((size_t)lo * p.Hv + hv) * (D * 4);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int at = n * C + 16 * r + lr;
-        const bool on = at < sg.rows;
-        const size_t tk = on ? token(at) : 0;
-        const int oc = col0 + 4 * NTW * g;
-        if (on) {
-          const size_t o = (tk * p.Hv + hv) * D + oc;
-          if (std::is_same<TO, float>::value || ro.out_f32) {
+        for (int r = 0; r < NR; ++r)
+          if (n * C + 16 * r + lr < sg.rows)
+            *reinterpret_cast<f32x4 *>(o + (__umul24(row_of(r), p.Hv * D * 4) + oc * 4)) = O[r];
+      } else {
+        char *o = static_cast<char *>(ro.out) + ((size_t)lo * p.Hv + hv) * (D * 2);
 #pragma unroll
-            for (int t = 0; t < NTW; ++t) *reinterpret_cast<f32x4 *>(static_cast<float *>(ro.out) + o + 4 * t) = O[t][r];
-          } else {
-            unsigned u[2 * NTW];
-#pragma unroll
-            for (int t = 0; t < NTW; ++t) {
-              u[2 * t] = pk_bf16(O[t][r][0], O[t][r][1]);
-              u[2 * t + 1] = pk_bf16(O[t][r][2], O[t][r][3]);
-            }
-            if constexpr (NTW == 2) *reinterpret_cast<uint4 *>(static_cast<__bf16 *>(ro.out) + o) = uint4{u[0], u[1], u[2], u[3]};
-            else *reinterpret_cast<uint2 *>(static_cast<__bf16 *>(ro.out) + o) = uint2{u[0], u[1]};
-          }
+        for (int r = 0; r < NR; ++r) {
+          const u32x2 u{pk_bf16(O[r][0], O[r][1]), pk_bf16(O[r][2], O[r][3])};
+          if (n * C + 16 * r + lr < sg.rows)
+            *reinterpret_cast<u32x2 *>(o + (__umul24(row_of(r), p.Hv * D * 2) + oc * 2)) = u;
         }
+      }
+      if constexpr (GRAD) {
         if (ro.dot) {   // uniform
-          float d = 0.f;
-          if (on) {
-            const TI *x = static_cast<const TI *>(ro.x) + (tk * (p.Hv / ro.gx) + hv / ro.gx) * D + oc;
+          f32x4 x[NR];
+          const int nx = p.Hv / ro.gx;
+          const char *q = static_cast<const char *>(ro.x) + ((size_t)lo * nx + hv / ro.gx) * (D * sizeof(TI));
 #pragma unroll
-            for (int t = 0; t < NTW; ++t)
+          for (int r = 0; r < NR; ++r)
+            x[r] = load4(reinterpret_cast<const TI *>(q + (__umul24(row_of(r), nx * D * (int)sizeof(TI)) + oc * (int)sizeof(TI))));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) d = fmaf(O[t][r][i], to_f32(x[4 * t + i]), d);
+          for (int r = 0; r < NR; ++r) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d = fmaf(O[r][i], x[r][i], d);
+            d += __shfl_xor(d, 16);
+            d += __shfl_xor(d, 32);
+            if (g == 0) dots[wave][16 * r + lr] = d;
           }
-          d += __shfl_xor(d, 16);
-          d += __shfl_xor(d, 32);
-          if (g == 0) dots[wave][16 * r + lr] = d;
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    asm volatile("" : "+v"(tr_c0), "+v"(tr_b));
     // the state
     const float e_end = fe[buf];
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
-      for (int t = 0; t < NTW; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) H[m][t][i] *= e_end;
+      for (int i = 0; i < 4; ++i) H[m][i] *= e_end;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      bf16x8 w[NTW][3];   // C's tokens 32 kb .. of the wave's columns, weighted
+      bf16x8 w[3];   // C's tokens 32 kb .. of the wave's columns, weighted
       float wt[8];
       ld8(&te[buf][32 * kb + 8 * g], wt);
+      bf16x8 cf[NPI];
 #pragma unroll
-      for (int t = 0; t < NTW; ++t) {
-        bf16x8 cf[NPI];
+      for (int k = 0; k < NPI; ++k) cf[k] = read_c(k, kb);
+      float x[8];
 #pragma unroll
-        for (int k = 0; k < NPI; ++k) cf[k] = read_tr(tr_c, k, kb, 4 * t);
-        float x[8];
+      for (int j = 0; j < 8; ++j) {
+        float v = (float)cf[0][j];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v = (float)cf[0][j];
-#pragma unroll
-          for (int k = 1; k < NPI; ++k) v += (float)cf[k][j];
-          x[j] = v * wt[j];
-        }
-        split8<3>(x, w[t]);
+        for (int k = 1; k < NPI; ++k) v += (float)cf[k][j];
+        x[j] = v * wt[j];
       }
-      // (operands read one tile ahead; scheduling fences keep the compiler from reading all of them at once)
-      bf16x8 f[2][NPI];
+      split8<3>(x, w);
+      asm volatile("" : "+v"(tr_b));
+      // two tiles of rows at a time, their operands read one pair ahead (the
+      // scheduling fences keep the compiler from reading all of them at once)
+      bf16x8 f[2][2][NPI];
+      auto read_pair = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < NPI; ++k) f[0][k] = read_tr(tr_b, k, kb, 0);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        if (m + 1 < 8)
+          for (int k = 0; k < NPI; ++k) f[m >> 1 & 1][j][k] = read_b(k, kb, m + j);
+      };
+      read_pair(0);
 #pragma unroll
-          for (int k = 0; k < NPI; ++k) f[(m + 1) & 1][k] = read_tr(tr_b, k, kb, 16 * (m + 1));
+      for (int m = 0; m < 8; m += 2) {
+        if (m + 2 < 8) read_pair(m + 2);
+        each_plane_pair<NPI, 3>([&](auto ka, auto kw) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < NTW; ++t) mma_planes<NPI, 3>(H[m][t], f[m & 1], w[t]);
+          for (int j = 0; j < 2; ++j)
+            H[m + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[m >> 1 & 1][j][ka], w[kw], H[m + j], 0, 0, 0);
+        });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     lds_barrier();
-    if constexpr (!FOLD) {
+    if constexpr (GRAD) {
       if (ro.dot && tid < C && n * C + tid < sg.rows)
-        ro.dot[(size_t)token(n * C + tid) * p.Hv + hv] = (dots[0][tid] + dots[1][tid]) + (dots[2][tid] + dots[3][tid]);
+        ro.dot[(size_t)token(n * C + tid) * p.Hv + hv] = sum_of<NW>([&](int w) { return dots[w][tid]; });
     }
     if (n + 1 < nch) store_chunk(n + 1);
     lds_barrier();
@@ -548,33 +642,36 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(LinArgs p) {
   auto store_state = [&](float *S) __attribute__((always_inline)) {
     const Place pl = state_place();
     const unsigned at = ro.trans ? pl.col * D + pl.row : pl.row * D + pl.col;
+    const unsigned dm = ro.trans ? 4 : 4 * D;   // rows: 32 (m / 2) + 4 (m % 2)
+    if (!ro.trans) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
+      for (int m = 0; m < 8; ++m) H[m] = quad_transpose(H[m], lane);
+    }
 #pragma unroll
-      for (int t = 0; t < NTW; ++t) {
-        const unsigned d = ro.trans ? 4 * t * D + 16 * m : 16 * m * D + 4 * t;
-        *reinterpret_cast<f32x4 *>(S + (at + d)) = ro.trans ? H[m][t] : quad_transpose(H[m][t], lane);
-      }
+    for (int m = 0; m < 8; ++m) *reinterpret_cast<f32x4 *>(S + (at + (8 * (m >> 1) + (m & 1)) * dm)) = H[m];
   };
   if constexpr (FOLD) {
     store_state(ro.fin + sth);
-    if (tid == 0 && col0 == 0) ro.dec[(size_t)sidx * p.Hv + hv] = decay_between(total, 0.);
+    if (tid == 64 * (NW - 1) && col0 < COLS) ro.dec[(size_t)sidx * p.Hv + hv] = decay_between(total, 0.);
   } else {
-    if (ro.fin && leaves) store_state(ro.fin + sqh);
-    if (ro.cross) {   // uniform
+    if (GRAD && ro.cross) {   // uniform
       const float *S = sg.last ? (ro.xs_last ? ro.xs_last + sqh : nullptr) : ro.xs + sth;
       float d = 0.f;
-      if (S)
-        load_state(S, [&](int m, int t, const f32x4 &x) {
+      if (S) {
+        f32x4 x[8];
+        load_state(S, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d = fmaf(H[m][t][i], x[i], d);
-        });
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d = fmaf(H[m][i], x[m][i], d);
+      }
 #pragma unroll
       for (int m = 32; m >= 1; m >>= 1) d += __shfl_xor(d, m);
       if (lane == 0) crs[wave] = d;
       __syncthreads();
-      if (tid == 0) ro.cross[(size_t)sidx * p.Hv + hv] = (crs[0] + crs[1]) + (crs[2] + crs[3]);
+      if (tid == 0) ro.cross[(size_t)sidx * p.Hv + hv] = sum_of<NW>([&](int w) { return crs[w]; });
     }
+    if (ro.fin && leaves) store_state(ro.fin + sqh);
   }
 }
 

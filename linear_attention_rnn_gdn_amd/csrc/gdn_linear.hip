@@ -13,19 +13,30 @@ using namespace gdn;
 
 namespace {
 
-// Tokens per segment: enough (segment, value head) walks to fill 256 compute
-// units twice, but no segment below kMinSegment tokens (each costs a state's
-// traffic, 64 KB written and read twice) nor, for the gradients, above
-// kMaxGradSegment (the decays' gradient is a sum over a segment).
-constexpr int kMinSegment = 256, kMaxGradSegment = 2048, kWalks = 512;
+// Tokens per segment: about kWalks (segment, value head) walks in all, one per
+// compute unit, but at least one chunk of tokens (two for the gradients), in
+// multiples of a chunk, and for the gradients kMaxGradSegment at most (the
+// decays' gradient is a sum over a segment).  A segment costs the fold's second
+// reading of k and v and a state's traffic (64 KB written, read and written by
+// the scan, read again); fewer walks leave compute units idle.  Measured, us a
+// call, bf16, 64 / 128 / 256 / 512 / 1024 / 2048 tokens per segment:
+//   forward, 4096 tokens x 32 heads   170 / 101 /  77 /  74 / 108 / 198 (512: 256 walks)
+//   forward, 2 x 8192 x 32            647 / 410 / 305 / 256 / 232 / 233 (2048)
+//   forward, 8192 x 4                  55 /  41 /  47 /  65 / 107 / 197 (128)
+//   forward, 2048 x 8                  32 /  36 /  42 /  62 / 106 / 128 (64)
+//   gradients, 4096 x 32              430 / 312 / 250 / 228 / 252 / 329
+//   gradients, 8192 x 4               115 /  89 /  86 / 103 / 163 / 294
+//   gradients, 2048 x 8                68 /  59 /  65 /  97 / 160 / 228
+constexpr int kWalks = 256, kMaxGradSegment = 2048;
 
 struct Plan {
   int L, J, nseg;   // tokens per segment, segments per sequence (padded batch), segments in all
 };
 Plan plan_of(const gdn_linear_shape &s, bool packed, bool grads) {
   const int64_t tokens = packed ? s.T : (int64_t)s.B * s.T;
+  const int64_t chunk = s.dtype == GDN_BF16 ? LinTile<__bf16>::C : LinTile<float>::C;
   int64_t L = (tokens * s.H_v + kWalks - 1) / kWalks;
-  L = std::max<int64_t>(kMinSegment, (L + 63) / 64 * 64);
+  L = std::max<int64_t>(std::max<int64_t>(64, grads ? 2 * chunk : chunk), (L + 63) / 64 * 64);
   if (grads) L = std::min<int64_t>(L, kMaxGradSegment);
   L = std::min<int64_t>(L, 1 << 30);
   Plan p{};
@@ -41,8 +52,8 @@ gdn_status validate_linear(const gdn_linear_shape *s, bool packed, bool grads) {
   if (s->o_dtype != GDN_F32 && s->o_dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (s->B < 1 || s->T < 0 || s->H_qk < 1 || s->H_v < 1 || s->H_v % s->H_qk) return GDN_ERR_SHAPE;
   if (s->d_k != D || s->d_v != D || (s->g_fixed & ~1)) return GDN_ERR_SHAPE;
-  if (s->H_v > (1 << 15) || (int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
-  // token indexes are 32-bit, and so are byte offsets within a chunk of 64 tokens; a segment's walks are 6 workgroups of a 1-D grid at most
+  if (s->H_v > (1 << 14) || (int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
+  // token indexes are 32-bit, and bytes between tokens fit 24; a segment's walks are 6 workgroups of a 1-D grid at most
   if (!packed && (int64_t)s->B * s->T > INT32_MAX) return GDN_ERR_SHAPE;
   const Plan p = plan_of(*s, packed, grads);
   if ((int64_t)p.nseg * s->H_v > (1 << 27)) return GDN_ERR_SHAPE;
@@ -87,10 +98,10 @@ LinLayout layout_linear(const gdn_linear_shape &s, bool packed, bool grads) {
   return L;
 }
 
-template <bool FOLD, int NTW, int NPO, typename TI, typename TO>
+template <int KIND, int NPO, typename TI, typename TO>
 gdn_status launch_walks(const LinArgs &a, hipStream_t st) {
-  const int64_t grid = (int64_t)a.nseg * a.Hv * a.roles * (2 / NTW);
-  hipLaunchKernelGGL((linear_kernel<FOLD, NTW, NPO, TI, TO>), dim3((unsigned)grid), dim3(256), 0, st, a);
+  const int64_t grid = (int64_t)a.nseg * a.Hv * a.roles;
+  hipLaunchKernelGGL((linear_kernel<KIND, 8, NPO, TI, TO>), dim3((unsigned)grid), dim3(512), 0, st, a);
   return check_launch();
 }
 
@@ -142,7 +153,7 @@ struct LinCall {
       a.role[0] = r;
       a.role[0].fin = reinterpret_cast<float *>(ws + L.add[0]);
       a.role[0].dec = reinterpret_cast<float *>(ws + L.dec[0]);
-      GDN_TRY((launch_walks<true, 2, 1, TI, float>(a, st)));
+      GDN_TRY((launch_walks<LIN_FOLD, 1, TI, float>(a, st)));
       ScanArgs sc{};
       sc.Hv = s.H_v; sc.J = p.J; sc.roles = 1;
       sc.seqs = cu ? reinterpret_cast<const int2 *>(ws + L.seqs) : nullptr;
@@ -152,8 +163,7 @@ struct LinCall {
     }
     r.init = h0; r.out = o; r.fin = h_T;
     a.role[0] = r;
-    if ((int64_t)p.nseg * s.H_v >= 256) return launch_walks<false, 2, NPO, TI, TO>(a, st);
-    return launch_walks<false, 1, NPO, TI, TO>(a, st);
+    return launch_walks<LIN_FWD, NPO, TI, TO>(a, st);
   }
 };
 
@@ -185,7 +195,7 @@ struct LinBwdCall {
         a.role[r].dec = fp(L.dec[r]);
         sc.role[r] = ScanRole{fp(L.add[r]), fp(L.dec[r]), r ? dh_T : f.h0, fp(L.x[r]), r};
       }
-      GDN_TRY((launch_walks<true, 2, 1, TI, float>(a, f.st)));
+      GDN_TRY((launch_walks<LIN_FOLD, 1, TI, float>(a, f.st)));
       GDN_TRY(launch_scan(s, sc, f.st));
     }
     const float *sx = s.T > p.L ? fp(L.x[0]) : nullptr, *dx = s.T > p.L ? fp(L.x[1]) : nullptr;
@@ -204,7 +214,7 @@ struct LinBwdCall {
     v.a = f.k; v.ga = R; v.b = f.q; v.gb = R; v.c = dO; v.gc = 1; v.rev = 1; v.gx = 1;
     v.init = dh_T; v.seg = dx; v.out = dv; v.fin = dh0;
     a.role[0] = q; a.role[1] = k; a.role[2] = v;
-    GDN_TRY((launch_walks<false, 2, 3, TI, TI>(a, f.st)));
+    GDN_TRY((launch_walks<LIN_GRAD, 3, TI, TI>(a, f.st)));
     const int64_t units = (int64_t)p.nseg * s.H_v;
     DgArgs d{};
     d.p = a; d.qd = fp(L.qd); d.kd = fp(L.kd); d.cross = fp(L.cross);

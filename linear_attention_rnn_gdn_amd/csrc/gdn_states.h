@@ -313,7 +313,21 @@ __global__ __launch_bounds__(256, (tree_wgs<MT, TI>())) void tree_kernel(StateAr
     for (int r = g; r < a.n; r += 4) put(r, z, z);
     return;
   }
-  // state columns: row 32 kb + 8 g + j, columns col .. col + NT - 1
+  // Everything that comes from memory is asked for before anything is waited
+  // for, without branches (an absent node's row, or one past the last, is
+  // dropped when it arrives): K and Q rows, V in the result layout, and the
+  // state's columns, row 32 kb + 8 g + j, columns col .. col + NT - 1.
+  constexpr int PER = 16 / sizeof(TI), PIECES = D / PER, LD = N * PIECES / 256;   // 16-byte pieces per row
+  static_assert(N * PIECES % 256 == 0, "whole pieces per thread");
+  const int pr = tid / PIECES, pc = (tid % PIECES) * PER;
+  u32x4 xk[LD], xq[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int r = min(pr + i * (256 / PIECES), a.n - 1);
+    const size_t at = (((size_t)b * a.n + r) * a.Hqk + hq) * D + pc;
+    xk[i] = *reinterpret_cast<const u32x4 *>(static_cast<const TI *>(a.k) + at);
+    xq[i] = *reinterpret_cast<const u32x4 *>(static_cast<const TI *>(a.q) + at);
+  }
   float s[4][8][NT];
   const float *S = a.state + ((size_t)slot * a.Hv + hv) * (D * D) + col;
 #pragma unroll
@@ -329,7 +343,15 @@ __global__ __launch_bounds__(256, (tree_wgs<MT, TI>())) void tree_kernel(StateAr
         s[kb][j][0] = *p;
       }
     }
-  // the tree (every wave its own copy), K and Q rows; absent nodes are zero
+  typedef TI VPart __attribute__((ext_vector_type(NT)));
+  VPart xv[MT][4];
+  const TI *vp = static_cast<const TI *>(a.v) + orow;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      xv[m][i] = *reinterpret_cast<const VPart *>(vp + (size_t)min(16 * m + 4 * g + i, a.n - 1) * ostep);
+  // the tree (every wave its own copy)
   const Path path = tree_path(a, b, hv, lane);
   const unsigned long long live = __ballot(path.live);
   if (wave == 0 && lane < N) {
@@ -337,17 +359,13 @@ __global__ __launch_bounds__(256, (tree_wgs<MT, TI>())) void tree_kernel(StateAr
     Al[lane] = path.live ? path.anc : 0ull;
     bl[lane] = DELTA && path.live ? a.beta[((size_t)b * a.n + lane) * a.Hv + hv] : 0.f;
   }
-  constexpr int PER = 16 / sizeof(TI), PIECES = D / PER;   // 16-byte pieces per row
-  for (int i = tid; i < N * PIECES; i += 256) {
-    const int r = i / PIECES, c = (i % PIECES) * PER;
-    uint4 xk{0, 0, 0, 0}, xq{0, 0, 0, 0};
-    if (live >> r & 1) {
-      const size_t at = (((size_t)b * a.n + r) * a.Hqk + hq) * D + c;
-      xk = *reinterpret_cast<const uint4 *>(static_cast<const TI *>(a.k) + at);
-      xq = *reinterpret_cast<const uint4 *>(static_cast<const TI *>(a.q) + at);
-    }
-    *reinterpret_cast<uint4 *>(kl + r * KP + c) = xk;
-    *reinterpret_cast<uint4 *>(ql + r * KP + c) = xq;
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int r = pr + i * (256 / PIECES);
+    const bool on = live >> r & 1;
+    const u32x4 z{0, 0, 0, 0};
+    *reinterpret_cast<u32x4 *>(kl + r * KP + pc) = on ? xk[i] : z;
+    *reinterpret_cast<u32x4 *>(ql + r * KP + pc) = on ? xq[i] : z;
   }
   __syncthreads();
   // 8 consecutive elements of an LDS row as operand planes
@@ -446,17 +464,17 @@ __global__ __launch_bounds__(256, (tree_wgs<MT, TI>())) void tree_kernel(StateAr
       for (int t = 0; t < NT; ++t) c[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], x[t][i], c[t], 0, 0, 0);
   };
   f32x4 U[MT][NT];
-  const TI *vp = static_cast<const TI *>(a.v) + orow;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     f32x4 R[NT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 16 * m + 4 * g + i;
-      float x[NT] = {};
-      if (live >> r & 1) {
+      float x[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = to_f32(vp[r * ostep + t]);
+      for (int t = 0; t < NT; ++t) {
+        const float v = (float)xv[m][i][t];
+        x[t] = live >> r & 1 ? v : 0.f;
       }
       const float er = decay_between(Gl[r], 0.), be = bl[r];
 #pragma unroll

@@ -395,7 +395,7 @@ def test_linear_calls_refuse_bad_arguments(abi):
         assert f(None, *good, ok, ws, null) == -1
         for bad, status in ((dict(B=0), -2), (dict(T=-1), -2), (dict(H_qk=0), -2), (dict(H_v=5), -2), (dict(d_k=64), -2),
                             (dict(d_v=256), -2), (dict(g_fixed=-1), -2), (dict(dtype=2), -3), (dict(o_dtype=7), -3),
-                            (dict(H_qk=1, H_v=(1 << 15) + 1), -2), (dict(B=1 << 25, T=1), -2)):
+                            (dict(H_qk=1, H_v=(1 << 14) + 1), -2), (dict(B=1 << 25, T=1), -2)):
             assert f(shape(**bad), *good, ok, big, null) == status, (kind, bad)
             with pytest.raises(abi.GdnError):
                 abi.workspace_size_linear(shape(**bad), kind)
@@ -405,7 +405,7 @@ def test_linear_calls_refuse_bad_arguments(abi):
 
 
 def test_linear_workspace_sizes(abi):
-    s = lambda **kw: abi.GdnLinearShape(*{**dict(B=1, T=200, H_qk=2, H_v=4, d_k=128, d_v=128, g_fixed=0, dtype=1, o_dtype=0),
+    s = lambda **kw: abi.GdnLinearShape(*{**dict(B=1, T=60, H_qk=2, H_v=4, d_k=128, d_v=128, g_fixed=0, dtype=1, o_dtype=0),
                                           **kw}.values())
     assert abi.workspace_size_linear(s(), abi.LINEAR_FWD) == 0            # one segment: no workspace
     assert abi.workspace_size_linear(s(T=20000), abi.LINEAR_FWD) > 0
