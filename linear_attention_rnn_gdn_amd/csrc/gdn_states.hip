@@ -11,6 +11,7 @@ using namespace gdn;
 
 namespace {
 
+constexpr int64_t kMemoryCache = 256 << 20;   // bytes of the memory-side cache
 constexpr int kMaxNodes = 64;   // tree nodes per row: one per lane of a wave
 
 gdn_status validate_pool(const gdn_pool_shape *s, bool slots) {
@@ -20,7 +21,7 @@ gdn_status validate_pool(const gdn_pool_shape *s, bool slots) {
   if (s->B < 1 || s->n < 1 || s->n > kMaxNodes || s->H_qk < 1 || s->H_v < 1 || s->H_v % s->H_qk) return GDN_ERR_SHAPE;
   if (s->d_k != D || s->d_v != D || s->n_slots < 1 || (s->g_fixed & ~1)) return GDN_ERR_SHAPE;
   if (!slots && s->n_slots < s->B) return GDN_ERR_SHAPE;
-  // (row, value head, column part) in a 1-D grid of at most 8 parts
+  // (row, value head, column part) in a 1-D grid of at most 4 parts
   if ((int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
@@ -28,14 +29,19 @@ gdn_status validate_pool(const gdn_pool_shape *s, bool slots) {
 StateArgs pool_args(const gdn_pool_shape &s) {
   StateArgs a{};
   a.B = s.B; a.n = s.n; a.Hqk = s.H_qk; a.Hv = s.H_v; a.n_slots = s.n_slots; a.g_fixed = s.g_fixed;
+  a.stream = (int64_t)s.B * s.H_v * D * D * 4 > kMemoryCache;
   return a;
 }
 
-// Columns of a state per workgroup of the step and of the commit.
-int state_cols(const gdn_pool_shape &s) {
-  const int64_t units = (int64_t)s.B * s.H_v;
-  return units >= 512 ? 128 : units >= 128 ? 64 : 32;
-}
+// Columns of a state per workgroup of the step and of the commit: a quarter of
+// a state where a call has few, to spread them over the chip, half of one else.
+// Measured, us a call with 16 / 32 / 64 / 128 columns per workgroup (step;
+// commit of 6 nodes), bf16:
+//     32 states   4.0 /  4.0 /  4.2 /  4.7;   4.8 /  5.0 /  5.4 /  6.3
+//    128 states   6.3 /  5.3 /  5.3 /  5.7;   7.0 /  6.4 /  6.5 /  7.3
+//    512 states  15.1 / 10.4 / 10.3 / 10.0;  16.8 / 13.6 / 12.6 / 12.7
+//   2048 states  47.9 / 42.5 / 41.0 / 41.9;  50.4 / 44.9 / 44.3 / 44.6
+bool quarter_states(const gdn_pool_shape &s) { return (int64_t)s.B * s.H_v < 128; }
 
 template <typename F>
 gdn_status with_types(const gdn_pool_shape &s, F &&f) {
@@ -56,6 +62,11 @@ gdn_status launch_commit(const StateArgs &a, hipStream_t st) {
   return check_launch();
 }
 
+// Two column tiles per wave (a workgroup takes a whole state, and a row's load
+// is a whole line) where there are two workgroups per compute unit then, one
+// (two workgroups per state) for fewer.  Measured, us a call of 16 nodes, one
+// tile / two: 256 states 7.5 / 7.6, 384 9.0 / 10.1, 512 12.7 / 12.2,
+// 1024 22.7 / 20.0, 2048 38.2 / 34.5.
 template <int MT, typename TI, typename TO, bool DELTA>
 gdn_status launch_tree(const StateArgs &a, hipStream_t st) {
   const int64_t units = (int64_t)a.B * a.Hv;
@@ -70,6 +81,7 @@ template <typename TI, typename TO, bool DELTA>
 gdn_status run_tree(const StateArgs &a, hipStream_t st) {
   if (a.n <= 16) return launch_tree<1, TI, TO, DELTA>(a, st);
   if (a.n <= 32) return launch_tree<2, TI, TO, DELTA>(a, st);
+  if (a.n <= 48) return launch_tree<3, TI, TO, DELTA>(a, st);
   return launch_tree<4, TI, TO, DELTA>(a, st);
 }
 
@@ -91,11 +103,7 @@ gdn_status gdn_step(const gdn_pool_shape *s, const void *q, const void *k, const
   return with_types(*s, [&](auto ti, auto to) -> gdn_status {
     using TI = decltype(ti);
     using TO = decltype(to);
-    switch (state_cols(*s)) {
-      case 128: return launch_step<128, TI, TO>(a, st);
-      case 64: return launch_step<64, TI, TO>(a, st);
-      default: return launch_step<32, TI, TO>(a, st);
-    }
+    return quarter_states(*s) ? launch_step<32, TI, TO>(a, st) : launch_step<64, TI, TO>(a, st);
   });
 }
 
@@ -131,11 +139,7 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *s, const void *k, const float *
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
   auto run = [&](auto ti) -> gdn_status {
     using TI = decltype(ti);
-    switch (state_cols(*s)) {
-      case 128: return launch_commit<128, TI>(a, st);
-      case 64: return launch_commit<64, TI>(a, st);
-      default: return launch_commit<32, TI>(a, st);
-    }
+    return quarter_states(*s) ? launch_commit<32, TI>(a, st) : launch_commit<64, TI>(a, st);
   };
   return s->dtype == GDN_BF16 ? run(__bf16{}) : run(float{});
 }
