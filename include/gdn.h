@@ -424,7 +424,9 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const flo
  *   g_fixed  0: log decays per token, g [B, T, H_v]; 1: one per value head,
  *            g [H_v]
  * Chunks and segments are the library's choice.  Limits: H_v <= 2^14,
- * B * H_v <= 2^26, B * T < 2^31.  A log decay of -inf (a hard reset) is allowed. */
+ * B * H_v <= 2^26, B * T < 2^31.  A log decay of -inf (a hard reset) is allowed.
+ * Outputs must not overlap inputs (h_T must not be h0: a sequence's segments
+ * run side by side). */
 typedef struct {
   int32_t B, T, H_qk, H_v, d_k, d_v, g_fixed;
   int32_t dtype, o_dtype;

@@ -672,6 +672,8 @@ def _linear_fwd(rows, cu, q, k, v, g, h0, o_dtype, output_final_state, workspace
         _check_tensors(dev, (out, "o", o_dtype, (B, T, Hv, dv)))
     if final_state is not None:
         _check_tensors(dev, (final_state, "h_T", torch.float32, state))
+        if h0 is not None and final_state.numel() and final_state.data_ptr() == h0.data_ptr():
+            raise ValueError("h_T must not be h0: a sequence's last segment may be written before its first is read")
     shape, need = _linear_plan(LINEAR_FWD if rows is None else LINEAR_VARLEN, n, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype),
                                _dt(o_dtype))
     with _on(dev, stream) as st:

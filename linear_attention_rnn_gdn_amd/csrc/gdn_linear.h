@@ -88,8 +88,8 @@ __device__ __forceinline__ Seg segment(const LinArgs &a, int s) {
 // [0, T]) are dropped, so no access leaves the tables.
 __global__ __launch_bounds__(256) void linear_table_kernel(const int *cu, int nseq, int T, int L, int nmax, int4 *tab,
                                                            int2 *seqs) {
-  __shared__ int part[257];
-  const int t = threadIdx.x;
+  __shared__ long long waves[4];
+  const int t = threadIdx.x, lane = t & 63;
   const int per = (nseq - 1) / 256 + 1;
   const int s0 = (int)min((int64_t)nseq, (int64_t)t * per), s1 = (int)min((int64_t)nseq, (int64_t)t * per + per);
   auto span = [&](int s, int &st, int &n) {
@@ -98,28 +98,30 @@ __global__ __launch_bounds__(256) void linear_table_kernel(const int *cu, int ns
     n = en - st;
     return n ? (n - 1) / L + 1 : 1;
   };
-  int mine = 0, st, n;
-  for (int s = s0; s < s1; ++s) mine = (int)min((int64_t)nmax, (int64_t)mine + span(s, st, n));
-  part[t] = mine;
-  __syncthreads();
-  if (t == 0) {
-    int run = 0;
-    for (int i = 0; i < 256; ++i) {
-      const int x = part[i];
-      part[i] = run;
-      run = (int)min((int64_t)nmax, (int64_t)run + x);
-    }
-    part[256] = run;
+  long long mine = 0;   // (64 bits: offsets that are no partition may add up to more than 32 hold)
+  int st, n;
+  for (int s = s0; s < s1; ++s) mine += span(s, st, n);
+  long long upto = mine;   // within the wave, then over the waves
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long long y = __shfl_up(upto, d);
+    if (lane >= d) upto += y;
   }
+  if (lane == 63) waves[t >> 6] = upto;
   __syncthreads();
-  int c = part[t];
+  long long before = upto - mine, total = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < t >> 6) before += waves[w];
+    total += waves[w];
+  }
+  int c = (int)min(before, (long long)nmax);
   for (int s = s0; s < s1; ++s) {
     const int ns = span(s, st, n), first = c;
     for (int j = 0; j < ns && c < nmax; ++j, ++c)
       tab[c] = int4{st + j * L, min(L, n - j * L), s, j | (j == ns - 1 ? 1 << 30 : 0)};
     seqs[s] = int2{first, c - first};
   }
-  for (int i = part[256] + t; i < nmax; i += 256) tab[i] = int4{0, -1, 0, 0};
+  for (int64_t i = total + t; i < nmax; i += 256) tab[i] = int4{0, -1, 0, 0};
 }
 
 // Transposition of a 4 x 4 block over the lanes 4 q .. 4 q + 3 and a tile's

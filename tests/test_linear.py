@@ -349,6 +349,38 @@ def test_workspace_holds_nothing_between_calls(gdn):
         gdn.linear_chunk_fwd(x["q"], x["k"], x["v"], x["g"], workspace=ws[:256])
 
 
+@pytest.mark.gpu
+def test_two_calls_at_once(gdn):
+    # forward and gradients of two problems on two streams, started together,
+    # against the same calls one after the other, bit for bit
+    xs = [_cuda(_draw(1, 1500 + 300 * i, 2, 4, "bf16", seed=20 + i, fixed=bool(i))) for i in range(2)]
+
+    def work(x, stream=None):
+        o, h = gdn.linear_chunk_fwd(x["q"], x["k"], x["v"], x["g"], x["h0"], stream=stream)
+        return [o, h] + list(gdn.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["dO"], x["h0"], x["dh_T"],
+                                                  stream=stream).values())
+
+    ref = [work(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = [work(x, s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_runs_agree_bit_for_bit(gdn):
+    # no atomics: the same call gives the same bits, whatever else ran before
+    x = _cuda(_draw(2, 777, 2, 6, "bf16", seed=31, fixed=True))
+    first = gdn.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["dO"], x["h0"], x["dh_T"])
+    for _ in range(3):
+        torch.randn(1 << 22, device="cuda").sum()
+        again = gdn.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["dO"], x["h0"], x["dh_T"])
+        assert all(torch.equal(again[n], first[n]) for n in first)
+
+
 # ---------------------------------------------------------------------------
 # refusals (no GPU needed: everything is rejected before a launch)
 
@@ -431,6 +463,8 @@ def test_linear_bindings_refuse_what_does_not_fit(gdn):
         gdn.linear_chunk_bwd(**args, dO=x["dO"].float())
     with pytest.raises(ValueError):
         gdn.linear_chunk_fwd(**args, h0=x["h0"][:1])
+    with pytest.raises(ValueError):   # the final state written over the initial one
+        gdn.linear_chunk_fwd(**args, h0=x["h0"], final_state=x["h0"])
     with pytest.raises(ValueError):
         gdn.linear_chunk_fwd_varlen(**args, cu_seqlens=[0, 40])
     one = {a: t[:1].contiguous() for a, t in args.items()}
