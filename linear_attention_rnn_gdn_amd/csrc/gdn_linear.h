@@ -49,6 +49,8 @@ struct LinArgs {
   int seg_len, J;             // tokens per segment, segments per sequence (padded batch)
   int nseg;                   // segments in all (packed: room for them)
   const int4 *tab;            // packed: (first token, tokens, sequence, segment of it | last << 30) per segment
+  const int *order;           // packed: the order in which segments are started
+  int alone;                  // packed: one workgroup per compute unit (for the launch)
   const float *g;             // log decays [tokens, H_v] or [H_v]
   int g_fixed;
   int roles;
@@ -85,9 +87,13 @@ __device__ __forceinline__ Seg segment(const LinArgs &a, int s) {
 // contiguous block of sequences.  Writes the segments' entries (those past
 // the last get rows = -1) and, per sequence, (first segment, segments).
 // Entries that would pass nmax (only for offsets that are no partition of
-// [0, T]) are dropped, so no access leaves the tables.
+// [0, T]) are dropped, so no access leaves the tables.  `order`: the segments
+// by their tokens, longest first (in 32 classes; within one in any order), in
+// which the walks are started: a long walk begun last would run alone.
 __global__ __launch_bounds__(256) void linear_table_kernel(const int *cu, int nseq, int T, int L, int nmax, int4 *tab,
-                                                           int2 *seqs) {
+                                                           int2 *seqs, int *order) {
+  constexpr int CLASSES = 32;
+  __shared__ int place[CLASSES + 1];
   __shared__ long long waves[4];
   const int t = threadIdx.x, lane = t & 63;
   const int per = (nseq - 1) / 256 + 1;
@@ -122,6 +128,23 @@ __global__ __launch_bounds__(256) void linear_table_kernel(const int *cu, int ns
     seqs[s] = int2{first, c - first};
   }
   for (int64_t i = total + t; i < nmax; i += 256) tab[i] = int4{0, -1, 0, 0};
+  // counting sort; class CLASSES: the entries past the last
+  if (t <= CLASSES) place[t] = 0;
+  __syncthreads();   // (the tables' entries too)
+  auto cls = [&](int i) { return i < total ? CLASSES - 1 - (int)min((int64_t)tab[i].y * CLASSES / L, (int64_t)CLASSES - 1) : CLASSES; };
+  for (int i = t; i < nmax; i += 256) atomicAdd(&place[cls(i)], 1);
+  __syncthreads();
+  if (t < 64) {
+    int v = t <= CLASSES ? place[t] : 0, w = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(w, d);
+      if (lane >= d) w += y;
+    }
+    if (t <= CLASSES) place[t] = w - v;
+  }
+  __syncthreads();
+  for (int i = t; i < nmax; i += 256) order[atomicAdd(&place[cls(i)], 1)] = i;
 }
 
 // Transposition of a 4 x 4 block over the lanes 4 q .. 4 q + 3 and a tile's
@@ -186,21 +209,6 @@ __device__ __forceinline__ f32x4 load4(const __bf16 *p) {
 template <typename TI> struct LinTile { static constexpr int C = 64, NPI = 1; };
 template <> struct LinTile<float> { static constexpr int C = 32, NPI = 3; };
 
-// NW waves; wave w holds 16 columns of the state, all 128 rows, in eight
-// result tiles.  Tile m's row 4 g + i is the state's row
-//   32 (m / 2) + 8 g + 4 (m % 2) + i,
-// so that a pair of tiles gives lane group g 8 consecutive rows: the pair is
-// the operand of the product with A's rows as these lie in memory.
-//
-// Per chunk: every wave multiplies its state (split into NPO planes) with all
-// rows of A (outputs transposed: state as the left operand, straight from its
-// result registers); the masked scores' 16 x 16 tiles are dealt out to the
-// waves, which leave them in LDS as NPO planes; after a barrier all waves add scores x C
-// for their columns, write their outputs, and add B^T (weighted C) to the
-// state (weighted C in three planes, so that the state keeps fp32 precision).
-// The chunk's operands sit in LDS in row-major order; products over tokens
-// read them with the transposing LDS read.  The next chunk's operands are
-// loaded into registers while this one is computed.
 // fn(i, j) for every pair of planes that mma_planes multiplies, in its order
 template <int NA, int NB, typename F>
 __device__ __forceinline__ void each_plane_pair(F &&fn) {
@@ -227,16 +235,47 @@ __device__ __forceinline__ float sum_of(F &&x) {
 }
 
 enum : int { LIN_FWD = 0, LIN_FOLD = 1, LIN_GRAD = 2 };
+constexpr int LIN_NW = 8;   // waves per workgroup
 // waves per SIMD that the registers are shared out for: two workgroups per
 // compute unit (one for fp32 inputs, whose planes fill more than half the LDS)
-template <typename TI, int NW> constexpr int lin_waves() { return std::is_same<TI, float>::value ? NW / 4 : NW / 2; }
-template <int KIND, int NW, int NPO, typename TI, typename TO>
-__global__ __launch_bounds__(64 * NW, (lin_waves<TI, NW>())) void linear_kernel(LinArgs p) {
+template <typename TI> constexpr int lin_waves() { return std::is_same<TI, float>::value ? LIN_NW / 4 : LIN_NW / 2; }
+// Eight waves; wave w holds 16 columns of the state, all 128 rows, in eight
+// result tiles.  Tile m's row 4 g + i is the state's row
+//   32 (m / 2) + 8 g + 4 (m % 2) + i,
+// so that a pair of tiles gives lane group g 8 consecutive rows: the pair is
+// the operand of the product with A's rows as these lie in memory.
+//
+// Per chunk: every wave multiplies its state (split into NPO planes) with all
+// rows of A (outputs transposed: state as the left operand, straight from its
+// result registers); the masked scores' 16 x 16 tiles are dealt out to the
+// waves, which leave them in LDS as NPO planes; after a barrier all waves add
+// scores x C for their columns, write their outputs, and add B^T (weighted C)
+// to the state.  The chunk's operands sit in LDS in row-major order; products
+// over tokens read them with the transposing LDS read.  The next chunk's
+// operands are loaded into registers while this one is computed.
+//
+// Roundings: decays are sums in fp64 and weights one exp2 of a rounded
+// difference; the state, the scores and all sums are fp32.  As operands the
+// weighted C goes in three planes (exact), state and scores in three where
+// the outputs are fp32 or feed the decays' gradient, in two where they are
+// rounded to bf16 anyway (2^-17 against the outputs' 2^-8; one plane would
+// add an error as large as the outputs' own).
+//
+// What bounds it (64 tokens x 128 x 128, bf16): 800 matrix-core instructions
+// of 16 cycles, 4300 vector and 900 LDS ones per chunk.  With every compute
+// unit busy a chunk takes about 10,000 cycles at one or at two workgroups per
+// unit, of which some instruction issues in 85%, vector ALU 58%, LDS 47%,
+// matrix cores 36%, and the clock falls to 1.9 GHz: it is bound by its
+// instructions, not by latency (doubling the LDS buffers, reading operands a
+// step ahead and loading two chunks ahead each changed nothing) nor by memory
+// (2 to 3 TB/s).  Measured: 4096 tokens x 32 heads in segments of 512, 48 us
+// (fold 24, scan 7).
+template <int KIND, int NPO, typename TI, typename TO>
+__global__ __launch_bounds__(64 * LIN_NW, lin_waves<TI>()) void linear_kernel(LinArgs p) {
   constexpr bool FOLD = KIND == LIN_FOLD, GRAD = KIND == LIN_GRAD;
   using L = LinTile<TI>;
   constexpr int C = L::C, NPI = L::NPI, NR = C / 16, KB = C / 32;
-  constexpr int NTHR = 64 * NW;
-  constexpr int COLS = 16 * NW;                   // state columns per workgroup
+  constexpr int NW = LIN_NW, NTHR = 64 * NW;
   constexpr int PER = 16 / sizeof(TI), PIECES = D / PER, ROWS = NTHR / PIECES, LD = C / ROWS;   // staging loads
   // operands, rows of 128 in 16-byte pieces; see piece_of()
   __shared__ __attribute__((aligned(256))) __bf16 al[FOLD ? 1 : NPI][FOLD ? 128 : C * D];
@@ -251,9 +290,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<TI, NW>())) void linear_kernel(
 
   int unit, part;
   const int R = p.Hv / p.Hqk;
-  xcd_unit(blockIdx.x, R * p.roles * (D / COLS), p.nseg * p.Hqk, unit, part);
-  const int sidx = unit / p.Hqk, hv = (unit % p.Hqk) * R + part / (p.roles * (D / COLS));
-  const int rn = part / (D / COLS) % p.roles;
+  xcd_unit(blockIdx.x, R * p.roles, p.nseg * p.Hqk, unit, part);
+  const int sidx = p.order ? p.order[unit / p.Hqk] : unit / p.Hqk, hv = (unit % p.Hqk) * R + part / p.roles;
+  const int rn = part % p.roles;
   // the role's fields, selected one by one: an indexed copy would sit in scratch memory
   LinRole ro;
 #define GDN_PICK(f) ro.f = rn == 0 ? p.role[0].f : rn == 1 ? p.role[1].f : p.role[2].f
@@ -261,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<TI, NW>())) void linear_kernel(
   GDN_PICK(init); GDN_PICK(seg); GDN_PICK(fin); GDN_PICK(dec); GDN_PICK(out); GDN_PICK(out_f32);
   GDN_PICK(x); GDN_PICK(gx); GDN_PICK(dot); GDN_PICK(xs); GDN_PICK(xs_last); GDN_PICK(cross);
 #undef GDN_PICK
-  const int col0 = (part % (D / COLS)) * COLS + 16 * wave;   // this wave's first column
+  const int col0 = 16 * wave;   // this wave's first column
   const Seg sg = segment(p, sidx);
   if (sg.rows < 0) return;
   const bool enters = ro.rev ? sg.last : sg.first, leaves = ro.rev ? sg.first : sg.last;
@@ -654,7 +693,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<TI, NW>())) void linear_kernel(
   };
   if constexpr (FOLD) {
     store_state(ro.fin + sth);
-    if (tid == 64 * (NW - 1) && col0 < COLS) ro.dec[(size_t)sidx * p.Hv + hv] = decay_between(total, 0.);
+    if (tid == 64 * (NW - 1)) ro.dec[(size_t)sidx * p.Hv + hv] = decay_between(total, 0.);
   } else {
     if (GRAD && ro.cross) {   // uniform
       const float *S = sg.last ? (ro.xs_last ? ro.xs_last + sqh : nullptr) : ro.xs + sth;

@@ -27,7 +27,7 @@ namespace {
 //   gradients, 4096 x 32              430 / 312 / 250 / 228 / 252 / 329
 //   gradients, 8192 x 4               115 /  89 /  86 / 103 / 163 / 294
 //   gradients, 2048 x 8                68 /  59 /  65 /  97 / 160 / 228
-constexpr int kWalks = 256, kMaxGradSegment = 2048;
+constexpr int kWalks = 256, kMaxGradSegment = 2048, kFewWalks = 4 * kWalks, kShort = 256, kLdsToBeAlone = 24 << 10;
 
 struct Plan {
   int L, J, nseg;   // tokens per segment, segments per sequence (padded batch), segments in all
@@ -61,7 +61,7 @@ gdn_status validate_linear(const gdn_linear_shape *s, bool packed, bool grads) {
 }
 
 struct LinLayout {
-  size_t tab, seqs, add[2], x[2], dec[2], qd, kd, cross, dq, dk, part, total;
+  size_t tab, seqs, order, add[2], x[2], dec[2], qd, kd, cross, dq, dk, part, total;
 };
 LinLayout layout_linear(const gdn_linear_shape &s, bool packed, bool grads) {
   const Plan p = plan_of(s, packed, grads);
@@ -76,6 +76,7 @@ LinLayout layout_linear(const gdn_linear_shape &s, bool packed, bool grads) {
   if (packed) {
     L.tab = take((size_t)p.nseg * sizeof(int4));
     L.seqs = take((size_t)s.B * sizeof(int2));
+    L.order = take((size_t)p.nseg * sizeof(int));
   }
   if (s.T > p.L) {
     for (int r = 0; r < (grads ? 2 : 1); ++r) {
@@ -101,7 +102,8 @@ LinLayout layout_linear(const gdn_linear_shape &s, bool packed, bool grads) {
 template <int KIND, int NPO, typename TI, typename TO>
 gdn_status launch_walks(const LinArgs &a, hipStream_t st) {
   const int64_t grid = (int64_t)a.nseg * a.Hv * a.roles;
-  hipLaunchKernelGGL((linear_kernel<KIND, 8, NPO, TI, TO>), dim3((unsigned)grid), dim3(512), 0, st, a);
+  const unsigned lds = KIND == LIN_FWD && a.alone ? kLdsToBeAlone : 0;
+  hipLaunchKernelGGL((linear_kernel<KIND, NPO, TI, TO>), dim3((unsigned)grid), dim3(64 * LIN_NW), lds, st, a);
   return check_launch();
 }
 
@@ -130,7 +132,17 @@ struct LinCall {
     LinArgs a{};
     a.Hqk = s.H_qk; a.Hv = s.H_v; a.T = s.T;
     a.seg_len = p.L; a.J = p.J; a.nseg = p.nseg;
+    // A few walks of packed sequences, whose lengths differ, run one workgroup
+    // per compute unit, by LDS asked for and not used: two would share the unit's
+    // instruction rate, and the longest first, one at a time, leave the least
+    // idle at the end (5 sequences of 1 .. 16000 tokens, 32 heads: 256 us, two
+    // per unit in the order of the batch 313; 16 of 1 .. 8192: 737, 760).  Many
+    // walks even out by themselves (256 sequences of 1 .. 300: 620 two per unit,
+    // 744 alone), and short ones are bound by their states' bytes (24 of
+    // 1 .. 200: 61, 70).
+    a.alone = cu && (int64_t)p.nseg * s.H_v <= kFewWalks && s.T / kShort >= s.B;
     a.tab = cu ? reinterpret_cast<const int4 *>(ws + L.tab) : nullptr;
+    a.order = cu ? reinterpret_cast<const int *>(ws + L.order) : nullptr;
     a.g = g; a.g_fixed = s.g_fixed;
     return a;
   }
@@ -142,7 +154,8 @@ struct LinCall {
     const int R = s.H_v / s.H_qk;
     if (cu) {
       hipLaunchKernelGGL(linear_table_kernel, dim3(1), dim3(256), 0, st, cu, s.B, s.T, p.L, p.nseg,
-                         reinterpret_cast<int4 *>(ws + L.tab), reinterpret_cast<int2 *>(ws + L.seqs));
+                         reinterpret_cast<int4 *>(ws + L.tab), reinterpret_cast<int2 *>(ws + L.seqs),
+                         reinterpret_cast<int *>(ws + L.order));
       GDN_TRY(check_launch());
     }
     LinArgs a = args(p, L);

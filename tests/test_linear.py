@@ -153,6 +153,23 @@ def test_forward_packed(gdn, lens, dtype, o_dtype, fixed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[900, 40, 300, 0, 1500, 700], [1, 199, 100, 0, 200] * 8])
+def test_forward_packed_many_heads(gdn, lens):
+    # few long walks (one workgroup per compute unit) and many short ones
+    Hqk, Hv = 16, 32
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    x = _draw(1, cu[-1], Hqk, Hv, "bf16", seed=len(lens), rows=len(lens))
+    o_ref, h_ref, _ = _reference(x, [(0, cu[i], cu[i + 1]) for i in range(len(lens))])
+    c = _cuda(x)
+    for turn in range(2):  # segments of one length start in any order: the results are the same
+        o, hT = gdn.linear_chunk_fwd_varlen(c["q"], c["k"], c["v"], c["g"], cu, c["h0"])
+        _check_fwd(o, hT, o_ref, h_ref, "bf16" if o.dtype == torch.bfloat16 else "f32")
+        if turn == 0:
+            first = o.clone(), hT.clone()
+    assert torch.equal(first[0], o) and torch.equal(first[1], hT)
+
+
+@pytest.mark.gpu
 def test_packed_offsets_that_are_no_partition_touch_nothing_else(gdn):
     # results are unspecified, but only the outputs may change: the inputs and
     # guard rows around the outputs keep their values
