@@ -707,10 +707,17 @@ def linear_chunk_fwd_varlen(q, k, v, g, cu_seqlens, h0=None, o_dtype=torch.float
     the batch dimension of q, k, v (and g) is 1; cu_seqlens as in
     chunk_fwd_varlen (n + 1 int32 offsets on the device, or a Python
     sequence); h0 and h_T [n,H_v,d_k,d_v]."""
-    if isinstance(k, torch.Tensor) and k.dim() == 4 and k.shape[0] != 1:
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a tensor")
+    if k.dim() == 4 and k.shape[0] != 1:
         raise ValueError("packed sequences: the batch dimension of q, k, v, g must be 1")
     if not isinstance(cu_seqlens, torch.Tensor):
-        cu_seqlens = torch.tensor(list(cu_seqlens), dtype=torch.int32, device=k.device)
+        if not k.is_cuda:
+            raise ValueError("k must be a device tensor")
+        # on the call's stream, so that the memory is not given to other work
+        # of the current stream while the call still reads it
+        with _on(k.device, stream):
+            cu_seqlens = torch.tensor(list(cu_seqlens), dtype=torch.int32, device=k.device)
     n = cu_seqlens.numel() - 1
     if n < 1:
         raise ValueError("cu_seqlens must hold at least two offsets")

@@ -388,6 +388,24 @@ def test_two_calls_at_once(gdn):
 
 
 @pytest.mark.gpu
+def test_offsets_of_a_call_on_another_stream(gdn):
+    # offsets given as a list belong to the call's stream: the current stream's
+    # next allocations must not get their memory while that stream is busy
+    lens = [300, 1, 700, 64]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    x = _cuda(_draw(1, cu[-1], 1, 2, "bf16", seed=41, rows=len(lens)))
+    ref = gdn.linear_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["g"], cu, x["h0"])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    got = gdn.linear_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["g"], cu, x["h0"], stream=s)
+    fill = [torch.zeros(len(cu), dtype=torch.int32, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert len(fill) == 8 and all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.gpu
 def test_runs_agree_bit_for_bit(gdn):
     # no atomics: the same call gives the same bits, whatever else ran before
     x = _cuda(_draw(2, 777, 2, 6, "bf16", seed=31, fixed=True))
