@@ -368,14 +368,14 @@ gdn_status gdn_chunk_fwd_noalloc(const gdn_shape *shape, const void *q, const vo
  * beta = NULL, linear attention with a decay per head (the same rule without
  * the correction):
  *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = S_t^T q_t.
- * B * H_v <= 2^26.  No workspace is used. */
+ * B * H_v <= 2^22.  No workspace is used.  Outputs must not overlap inputs. */
 typedef struct {
   int32_t B, n, H_qk, H_v, d_k, d_v, n_slots, g_fixed;
   int32_t dtype, o_dtype;
 } gdn_pool_shape;
 
 /* One token of every row: the recurrent form of gdn_chunk_fwd (and of
- * gdn_linear_fwd) for decoding.  Each row's state is advanced in place and
+ * gdn_linear_chunk_fwd) for decoding.  Each row's state is advanced in place and
  * read with q.
  *   q, k [B, H_qk, d_k], v [B, H_v, d_v] dtype; g [B, H_v] or [H_v] fp32;
  *   beta [B, H_v] fp32 or NULL (the linear rule); state: the pool (read and
@@ -390,7 +390,8 @@ gdn_status gdn_step(const gdn_pool_shape *shape, const void *q, const void *k, c
  * ancestors first (parents[r] < r); a node with any other value of parents,
  * or with an ancestor that has one, is absent: its outputs are zero, its
  * inputs are not read into any result.  The pool is only read, so rows may
- * share a slot (drafts forked from one sequence).
+ * share a slot (drafts forked from one sequence).  An infinity or NaN in a
+ * node that is not absent may reach any node of its row.
  *   q, k [B, n, H_qk, d_k], v [B, n, H_v, d_v] dtype; g [B, n, H_v] or [H_v],
  *   beta [B, n, H_v] fp32 or NULL (the linear rule); parents [B, n] int32;
  *   o [B, n, H_v, d_v] o_dtype, u [B, n, H_v, d_v] fp32 (written): u are the
@@ -424,7 +425,10 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const flo
  *   g_fixed  0: log decays per token, g [B, T, H_v]; 1: one per value head,
  *            g [H_v]
  * Chunks and segments are the library's choice.  Limits: H_v <= 2^14,
- * B * H_v <= 2^26, B * T < 2^31.  A log decay of -inf (a hard reset) is allowed.
+ * B * H_v <= 2^18, B * T < 2^31, for gradients B * T * H_v <= 2^31.  A log
+ * decay of -inf (a hard reset) is allowed.  An infinity or NaN in a token's q,
+ * k or v may also reach the outputs of the up to 63 tokens before it that share
+ * its chunk, never another sequence's.
  * Outputs must not overlap inputs (h_T must not be h0: a sequence's segments
  * run side by side). */
 typedef struct {

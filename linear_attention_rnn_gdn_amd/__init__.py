@@ -658,7 +658,7 @@ def _linear_inputs(q, k, v, g):
 def _workspace(workspace, need, dev):
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _check_tensors(dev, (workspace, "workspace", torch.uint8, (workspace.numel(),)))
+    _need(workspace, "workspace", torch.uint8, None, dev)
     return workspace
 
 

@@ -52,11 +52,14 @@ gdn_status validate_linear(const gdn_linear_shape *s, bool packed, bool grads) {
   if (s->o_dtype != GDN_F32 && s->o_dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (s->B < 1 || s->T < 0 || s->H_qk < 1 || s->H_v < 1 || s->H_v % s->H_qk) return GDN_ERR_SHAPE;
   if (s->d_k != D || s->d_v != D || (s->g_fixed & ~1)) return GDN_ERR_SHAPE;
-  if (s->H_v > (1 << 14) || (int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
-  // token indexes are 32-bit, and bytes between tokens fit 24; a segment's walks are 6 workgroups of a 1-D grid at most
+  // a launch holds fewer than 2^32 threads: the scan has 16 workgroups of 256 per
+  // sequence, value head and role (2 for gradients), the walks one of 512 per
+  // segment, value head and role (3)
+  if (s->H_v > (1 << 14) || (int64_t)s->B * s->H_v > (1 << 18)) return GDN_ERR_SHAPE;
+  // token indexes are 32-bit, and bytes between tokens fit 24
   if (!packed && (int64_t)s->B * s->T > INT32_MAX) return GDN_ERR_SHAPE;
   const Plan p = plan_of(*s, packed, grads);
-  if ((int64_t)p.nseg * s->H_v > (1 << 27)) return GDN_ERR_SHAPE;
+  if ((int64_t)p.nseg * s->H_v > (1 << 21)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 

@@ -21,8 +21,8 @@ gdn_status validate_pool(const gdn_pool_shape *s, bool slots) {
   if (s->B < 1 || s->n < 1 || s->n > kMaxNodes || s->H_qk < 1 || s->H_v < 1 || s->H_v % s->H_qk) return GDN_ERR_SHAPE;
   if (s->d_k != D || s->d_v != D || s->n_slots < 1 || (s->g_fixed & ~1)) return GDN_ERR_SHAPE;
   if (!slots && s->n_slots < s->B) return GDN_ERR_SHAPE;
-  // (row, value head, column part) in a 1-D grid of at most 4 parts
-  if ((int64_t)s->B * s->H_v > (1 << 26)) return GDN_ERR_SHAPE;
+  // a launch holds fewer than 2^32 threads: at most 2 workgroups of 256 per state here
+  if ((int64_t)s->B * s->H_v > (1 << 22)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 

@@ -406,6 +406,27 @@ def test_offsets_of_a_call_on_another_stream(gdn):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,C", [("bf16", 64), ("f32", 32)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_stay_in_their_sequence(gdn, dtype, C, bad):
+    # tokens 210 .. of the middle sequence, and what lies behind the last one:
+    # the other sequences, and the chunks before, keep their bits
+    lens, at = [70, 401, 33], 210
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    x = _cuda(_draw(1, cu[-1] + 50, 1, 2, dtype, seed=51, rows=len(lens)))
+    o, h = gdn.linear_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["g"], cu, x["h0"], o_dtype=DT[dtype])
+    y = {n: t.clone() for n, t in x.items()}
+    for n in ("q", "k", "v"):
+        y[n][0, cu[1] + at:cu[2]] = bad
+        y[n][0, cu[3]:] = bad
+    o2, h2 = gdn.linear_chunk_fwd_varlen(y["q"], y["k"], y["v"], y["g"], cu, x["h0"], o_dtype=DT[dtype])
+    assert torch.equal(o2[0, :cu[1] + at // C * C], o[0, :cu[1] + at // C * C])
+    assert torch.equal(o2[0, cu[2]:cu[3]], o[0, cu[2]:cu[3]])
+    assert torch.equal(h2[[0, 2]], h[[0, 2]])
+    assert not torch.isfinite(o2[0, cu[1] + at:cu[2]]).any() and not torch.isfinite(h2[1]).any()
+
+
+@pytest.mark.gpu
 def test_runs_agree_bit_for_bit(gdn):
     # no atomics: the same call gives the same bits, whatever else ran before
     x = _cuda(_draw(2, 777, 2, 6, "bf16", seed=31, fixed=True))
@@ -507,3 +528,17 @@ def test_linear_bindings_refuse_what_does_not_fit(gdn):
         gdn.linear_chunk_fwd_varlen(**one, cu_seqlens=[0])
     with pytest.raises(TypeError):
         gdn.linear_chunk_fwd_varlen(**one, cu_seqlens=torch.tensor([0, 40], device="cuda"))
+
+
+def test_linear_sizes_that_no_launch_holds_are_refused(abi):
+    # a launch holds fewer than 2^32 threads: 16 workgroups of 256 per state and
+    # role in the scan, one of 512 per walk
+    at = dict(B=1 << 16, T=1, H_qk=2, H_v=4, d_k=128, d_v=128, g_fixed=0, dtype=1, o_dtype=0)
+    for kind in (abi.LINEAR_FWD, abi.LINEAR_VARLEN, abi.LINEAR_BWD):
+        abi.workspace_size_linear(abi.GdnLinearShape(*at.values()), kind)
+        with pytest.raises(abi.GdnError):
+            abi.workspace_size_linear(abi.GdnLinearShape(*{**at, "B": (1 << 16) + 1}.values()), kind)
+    long = dict(at, B=1, T=(1 << 29) - 1)   # B T H_v just below 2^31
+    abi.workspace_size_linear(abi.GdnLinearShape(*long.values()), abi.LINEAR_BWD)
+    with pytest.raises(abi.GdnError):
+        abi.workspace_size_linear(abi.GdnLinearShape(*{**long, "H_v": 64}.values()), abi.LINEAR_BWD)

@@ -416,6 +416,17 @@ def test_pool_calls_refuse_bad_arguments(abi):
     assert L.gdn_step(shape(n=2), *([ok] * 8), null) == -2
 
 
+def test_pool_sizes_that_no_launch_holds_are_refused(abi):
+    # a launch holds fewer than 2^32 threads: two workgroups of 256 per state;
+    # pointers that are refused later tell the largest size from one past it
+    L = abi.lib()
+    odd = (1 << 20) + 4
+    for f, count in ((L.gdn_step, 8), (L.gdn_tree_fwd, 10), (L.gdn_tree_commit, 7)):
+        for B, status in ((1 << 20, -4), ((1 << 20) + 1, -2)):
+            shape = abi.GdnPoolShape(B, 1, 2, 4, 128, 128, 1 << 21, 0, 1, 0)
+            assert f(shape, *([odd] * count), None) == status
+
+
 def test_pool_bindings_refuse_host_tensors(abi):
     x = _draw(2, None, 1, 2, 2, "bf16", seed=1)
     with pytest.raises(ValueError):
