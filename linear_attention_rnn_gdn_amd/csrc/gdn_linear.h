@@ -268,8 +268,8 @@ template <typename TI> constexpr int lin_waves() { return std::is_same<TI, float
 // matrix cores 36%, and the clock falls to 1.9 GHz: it is bound by its
 // instructions, not by latency (doubling the LDS buffers, reading operands a
 // step ahead and loading two chunks ahead each changed nothing) nor by memory
-// (2 to 3 TB/s).  Measured: 4096 tokens x 32 heads in segments of 512, 48 us
-// (fold 24, scan 7).
+// (2 to 3 TB/s).  Measured: 4096 tokens x 32 heads in segments of 512, 49 us
+// (fold 25, scan 7).
 template <int KIND, int NPO, typename TI, typename TO>
 __global__ __launch_bounds__(64 * LIN_NW, lin_waves<TI>()) void linear_kernel(LinArgs p) {
   constexpr bool FOLD = KIND == LIN_FOLD, GRAD = KIND == LIN_GRAD;
