@@ -408,6 +408,8 @@ gdn_status gdn_tree_fwd(const gdn_pool_shape *shape, const void *q, const void *
  * a = last[b], G the sum of the log decays along a node's path, u from
  * gdn_tree_fwd (same k, g, parents).  last[b] outside [0, n) (nothing was
  * accepted) or an absent node leaves the row's state as it is.
+ * Such a row writes no state and claims no slot: of rows that name one slot
+ * (drafts forked from one sequence) the first one that commits a node is run.
  *   k [B, n, H_qk, d_k] dtype, u [B, n, H_v, d_v] fp32, g as above, parents
  *   [B, n], last [B] int32.  shape->o_dtype is not used. */
 gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const float *u,

@@ -604,9 +604,10 @@ def tree_fwd(q, k, v, g, beta, parents, state, slots=None, o_dtype=torch.float32
 
 def tree_commit(k, u, g, parents, last, state, slots=None, stream=None):
     """The commit of an accepted path (gdn_tree_commit): row b's state becomes
-    the state of node last[b], in place (last[b] outside the tree: left as it
-    is).  k, g, parents as given to tree_fwd, u as returned by it; last [B]
-    int32.  Rows naming one slot: the first is run.  Returns state."""
+    the state of node last[b], in place (last[b] outside the tree, or an absent
+    node: nothing is committed and the state is left as it is).  k, g, parents
+    as given to tree_fwd, u as returned by it; last [B] int32.  Rows naming one
+    slot: the first one that commits a node is run.  Returns state."""
     B, n, Hqk, Hv, dk, dv, n_slots, dev, items = _pool_dims(k, u, state, slots, 2)
     fixed, gshape = _decay_shape(g, (B, n, Hv))
     _check_tensors(dev, *items, (u, "u", torch.float32, (B, n, Hv, dv)), (g, "g", torch.float32, gshape),

@@ -34,11 +34,13 @@ __device__ __forceinline__ int row_slot(const StateArgs &a, int b) {
   return s >= 0 && s < a.n_slots ? s : -1;
 }
 
-// Whether an earlier row names the same slot (a thread's share of the rows).
-__device__ __forceinline__ bool slot_seen(const StateArgs &a, int b, int slot, int tid, int nthreads) {
+// Whether an earlier row that writes names the same slot (a thread's share of
+// the rows); writes(i): row i writes the state of the slot it names.
+template <typename F>
+__device__ __forceinline__ bool slot_seen(const StateArgs &a, int b, int slot, int tid, int nthreads, F &&writes) {
   bool seen = false;
   if (a.slots)
-    for (int i = tid; i < b; i += nthreads) seen |= a.slots[i] == slot;
+    for (int i = tid; i < b; i += nthreads) seen |= a.slots[i] == slot && writes(i);
   return seen;
 }
 
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(256) void step_kernel(StateArgs a) {
   const float eg = decay_between(log2_decay(a.g[a.g_fixed ? hv : (size_t)b * a.Hv + hv]), 0.);
   const float beta = a.beta ? a.beta[(size_t)b * a.Hv + hv] : 0.f;
   __syncthreads();
-  if (slot_seen(a, b, slot, tid, 256)) dup = 1;
+  if (slot_seen(a, b, slot, tid, 256, [](int) { return true; })) dup = 1;
   float kr[RPT];
   float4 sk{0.f, 0.f, 0.f, 0.f}, sq{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -194,12 +196,28 @@ __device__ __forceinline__ Path tree_path(const StateArgs &a, int b, int hv, int
 }
 
 // ----------------------------------------------------------------------------
+// Whether row b commits something: its last node lies in the tree, and it and
+// all its ancestors are present.  One thread, at most 64 steps.
+__device__ __forceinline__ bool row_commits(const StateArgs &a, int b) {
+  int at = a.last[b];
+  if (at < 0 || at >= a.n) return false;
+  while (at >= 0) {
+    const int p = a.parents[(size_t)b * a.n + at];
+    if (p < -1 || p >= at) return false;
+    at = p;
+  }
+  return true;
+}
+
 // The accepted path's commit:  S' = e^{G_a} S + sum_{i on the path to a}
 // e^{G_a - G_i} k_i u_i^T, with u_i the corrected values of the check: a
 // rank-(path length) update, 2 x 64 KB of state traffic per row and head, so
 // it is laid out as the step (each thread RPT rows of 4 columns) and the
 // path's k and u pass through LDS in batches of 8 nodes, weights folded into
-// k.  All sums are fp32.
+// k.  All sums are fp32.  Of the rows that name a slot the first one that
+// commits something is run: an earlier row's path is looked at only where its
+// slot is this one (forks of one sequence), so other calls pay for the slots'
+// comparison alone.
 template <int COLS, typename TI>
 __global__ __launch_bounds__(256) void tree_commit_kernel(StateArgs a) {
   constexpr int LPR = COLS / 4, RG = 256 / LPR, RPT = D / RG, NB = 8;
@@ -225,7 +243,7 @@ __global__ __launch_bounds__(256) void tree_commit_kernel(StateArgs a) {
   const float w = decay_between(Ga, t.G);   // this lane's node's weight, if it is on the path
   const float ea = decay_between(Ga, 0.);
   __syncthreads();
-  if (slot_seen(a, b, slot, tid, 256)) dup = 1;
+  if (slot_seen(a, b, slot, tid, 256, [&](int i) { return row_commits(a, i); })) dup = 1;
   __syncthreads();
   if (dup || !live) return;   // uniform
 #pragma unroll
