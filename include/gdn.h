@@ -431,8 +431,9 @@ gdn_status gdn_tree_commit(const gdn_pool_shape *shape, const void *k, const flo
  * decay of -inf (a hard reset) is allowed.  An infinity or NaN in a token's q,
  * k or v may also reach the outputs of the up to 63 tokens before it that share
  * its chunk, never another sequence's.
- * Outputs must not overlap inputs (h_T must not be h0: a sequence's segments
- * run side by side). */
+ * Outputs must not overlap inputs or each other (h_T must not be h0: a
+ * sequence's segments run side by side; nor may dh0 be h0 or dh_T: the
+ * gradients' walks read those beside the one that writes dh0). */
 typedef struct {
   int32_t B, T, H_qk, H_v, d_k, d_v, g_fixed;
   int32_t dtype, o_dtype;

@@ -20,6 +20,8 @@ States in a pool [n_slots,H_v,d_k,d_v], for serving (beta=None: the linear rule)
   step(q, k, v, g, beta, state, slots=None)                     -> o
   tree_fwd(q, k, v, g, beta, parents, state, slots=None)        -> (o, u)
   tree_commit(k, u, g, parents, last, state, slots=None)        -> state
+Outputs and a workspace that a caller passes to these (out, final_state,
+values, workspace) are refused where they overlap an input or each other.
 """
 from __future__ import annotations
 
@@ -520,6 +522,26 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _check_apart(outputs, inputs):
+    """Outputs (and a workspace) that the caller passed must lie apart from
+    the inputs and from each other: workgroups that still read an input run
+    beside those that write.  Both are (tensor or None, name) pairs of
+    contiguous tensors."""
+    def span(t, name):
+        at = t.data_ptr()
+        return at, at + t.numel() * t.element_size(), name
+
+    taken = [span(t, name) for t, name in inputs if t is not None and t.numel()]
+    for t, name in outputs:
+        if t is None or not t.numel():
+            continue
+        lo, hi, _ = here = span(t, name)
+        for a, b, other in taken:
+            if a < hi and lo < b:
+                raise ValueError(f"{name} overlaps {other}")
+        taken.append(here)
+
+
 @functools.lru_cache(maxsize=256)
 def _pool_shape(*sizes):
     return GdnPoolShape(*sizes)
@@ -564,6 +586,8 @@ def step(q, k, v, g, beta, state, slots=None, o_dtype=torch.float32, out=None, s
     if out is not None:
         items.append((out, "o", o_dtype, (B, Hv, dv)))
     _check_tensors(dev, *items)
+    if out is not None:
+        _check_apart(((out, "o"),), ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state"), (slots, "slots")))
     shape = _pool_shape(B, 1, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
     with _on(dev, stream) as st:
         o = out if out is not None else torch.empty((B, Hv, dv), dtype=o_dtype, device=dev)
@@ -593,6 +617,10 @@ def tree_fwd(q, k, v, g, beta, parents, state, slots=None, o_dtype=torch.float32
     if values is not None:
         items.append((values, "u", torch.float32, (B, n, Hv, dv)))
     _check_tensors(dev, *items)
+    if not (out is None and values is None):
+        _check_apart(((out, "o"), (values, "u")),
+                     ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (parents, "parents"), (state, "state"),
+                      (slots, "slots")))
     shape = _pool_shape(B, n, Hqk, Hv, dk, dv, n_slots, fixed, _dt(k.dtype), _dt(o_dtype))
     with _on(dev, stream) as st:
         o = out if out is not None else torch.empty((B, n, Hv, dv), dtype=o_dtype, device=dev)
@@ -656,13 +684,6 @@ def _linear_inputs(q, k, v, g):
     return B, T, Hqk, Hv, dk, dv, fixed, dev
 
 
-def _workspace(workspace, need, dev):
-    if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, None, dev)
-    return workspace
-
-
 def _linear_fwd(rows, cu, q, k, v, g, h0, o_dtype, output_final_state, workspace, out, final_state, stream):
     B, T, Hqk, Hv, dk, dv, fixed, dev = _linear_inputs(q, k, v, g)
     n = B if rows is None else rows
@@ -673,12 +694,15 @@ def _linear_fwd(rows, cu, q, k, v, g, h0, o_dtype, output_final_state, workspace
         _check_tensors(dev, (out, "o", o_dtype, (B, T, Hv, dv)))
     if final_state is not None:
         _check_tensors(dev, (final_state, "h_T", torch.float32, state))
-        if h0 is not None and final_state.numel() and final_state.data_ptr() == h0.data_ptr():
-            raise ValueError("h_T must not be h0: a sequence's last segment may be written before its first is read")
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    if not (out is None and final_state is None and workspace is None):
+        _check_apart(((out, "o"), (final_state, "h_T"), (workspace, "workspace")),
+                     ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (h0, "h0"), (cu, "cu_seqlens")))
     shape, need = _linear_plan(LINEAR_FWD if rows is None else LINEAR_VARLEN, n, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype),
                                _dt(o_dtype))
     with _on(dev, stream) as st:
-        ws = _workspace(workspace, need, dev)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
         o = out if out is not None else torch.empty((B, T, Hv, dv), dtype=o_dtype, device=dev)
         hT = None
         if output_final_state:
@@ -743,9 +767,14 @@ def linear_chunk_bwd(q, k, v, g, dO, h0=None, dh_T=None, workspace=None, out=Non
     if out is not None:
         for name, (dt, sh) in want.items():
             _check_tensors(dev, (out[name], name, dt, sh))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    if not (out is None and workspace is None):
+        _check_apart([(out[name], name) for name in want if out is not None] + [(workspace, "workspace")],
+                     ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (dO, "dO"), (h0, "h0"), (dh_T, "dh_T")))
     shape, need = _linear_plan(LINEAR_BWD, B, T, Hqk, Hv, dk, dv, fixed, _dt(k.dtype), F32)
     with _on(dev, stream) as st:
-        ws = _workspace(workspace, need, dev)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
         if out is None:
             out = {name: torch.empty(sh, dtype=dt, device=dev) for name, (dt, sh) in want.items()}
         _check(lib().gdn_linear_chunk_bwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(h0), _addr(dO),
