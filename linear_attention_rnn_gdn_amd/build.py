@@ -10,10 +10,6 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_api.hip"), os.path.join(CSRC, "gdn_states.hip"),
            os.path.join(CSRC, "gdn_linear.hip")]
-HEADERS = [os.path.join(CSRC, "gdn_kernels.h"), os.path.join(CSRC, "gdn_mfma.h"),
-           os.path.join(CSRC, "gdn_common.h"), os.path.join(CSRC, "gdn_host.h"),
-           os.path.join(CSRC, "gdn_states.h"),
-           os.path.join(CSRC, "gdn_linear.h"), os.path.join(ROOT, "include", "gdn.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
