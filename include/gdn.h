@@ -474,9 +474,11 @@ gdn_status gdn_linear_chunk_fwd_varlen(const gdn_linear_shape *shape, const int3
  *   dv [B, T, H_v, d_v] dtype, each rounded once from fp32; dg fp32, shaped
  *   as g (fixed decays: the sum over all tokens); dh0 [B, H_v, d_k, d_v] fp32
  *   or NULL.  shape->o_dtype is not used.
- * dg is formed from differences <q_t, dq_t> - <k_t, dk_t>: its error is about
- * 1e-6 of |q_t| |dq_t| + |k_t| |dk_t|, also where decays are so strong that dg
- * itself is far smaller. */
+ * dg_t is a sum of differences <q_s, dq_s> - <k_s, dk_s> over the tokens s >= t
+ * of t's segment (2048 at most, the library's choice) and of <S, dS> at its
+ * end: its error is about 1e-6 of the largest |q_s| |dq_s| + |k_s| |dk_s| and
+ * |S| |dS| among them, also where decays are so strong, or t's own terms so
+ * small, that dg_t itself is far smaller. */
 gdn_status gdn_linear_chunk_bwd(const gdn_linear_shape *shape, const void *q, const void *k,
                                 const void *v, const float *g, const float *h0, const void *dO,
                                 const float *dh_T, void *dq, void *dk, void *dv, float *dg,

@@ -56,8 +56,13 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&f)[NP]) {
 }
 
 // c += A B over the planes of both operands, the products of planes i and j
-// with i + j < max(NA, NB), smallest first: what is left out is below the
-// precision of the operand with more planes.
+// with i + j < max(NA, NB), smallest first.  What is left out, of a product
+// x y: nothing where one operand is one plane and exact (bf16 inputs); with
+// three planes of both, x1 y2 + x2 y1 + x2 y2, where cut planes obey
+// |x1| < 2^-7 |x| and |x2| < 2^-15 |x|: less than 2^-21 |x y|, always with the
+// product's own sign (cutting keeps it).  In a sum that is at most 2^-21 of the
+// sum of the terms' sizes: 8 roundings of fp32, and no more than the fp32 sum
+// of a few dozen terms itself loses.
 template <int NA, int NB>
 __device__ __forceinline__ void mma_planes(f32x4 &c, const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]) {
   constexpr int M = NA > NB ? NA : NB;

@@ -203,9 +203,10 @@ __device__ __forceinline__ f32x4 load4(const __bf16 *p) {
 }
 
 // How a walk is laid out for inputs of type TI: C tokens per chunk and planes
-// per input value.  fp32 inputs: three bf16 planes hold every bit, so all
-// products run on the bf16 matrix cores (6 of their passes against the 16
-// times slower fp32 instruction), with half the chunk to fit the LDS.
+// per input value.  fp32 inputs: three bf16 planes hold every bit (their
+// products leave out 2^-21 at most, see mma_planes), so all products run on
+// the bf16 matrix cores (6 of their passes against the 16 times slower fp32
+// instruction), with half the chunk to fit the LDS.
 template <typename TI> struct LinTile { static constexpr int C = 64, NPI = 1; };
 template <> struct LinTile<float> { static constexpr int C = 32, NPI = 3; };
 
@@ -237,7 +238,9 @@ __device__ __forceinline__ float sum_of(F &&x) {
 enum : int { LIN_FWD = 0, LIN_FOLD = 1, LIN_GRAD = 2 };
 constexpr int LIN_NW = 8;   // waves per workgroup
 // waves per SIMD that the registers are shared out for: two workgroups per
-// compute unit (one for fp32 inputs, whose planes fill more than half the LDS)
+// compute unit for bf16 inputs, one for fp32 ones, for the gradients' sake
+// (81,960 bytes of LDS, 40 more than half of it, and 137 registers).  The fp32
+// forward takes 80,904 bytes and 126 registers, so that two fit all the same.
 template <typename TI> constexpr int lin_waves() { return std::is_same<TI, float>::value ? LIN_NW / 4 : LIN_NW / 2; }
 // Eight waves; wave w holds 16 columns of the state, all 128 rows, in eight
 // result tiles.  Tile m's row 4 g + i is the state's row
@@ -256,20 +259,26 @@ template <typename TI> constexpr int lin_waves() { return std::is_same<TI, float
 //
 // Roundings: decays are sums in fp64 and weights one exp2 of a rounded
 // difference; the state, the scores and all sums are fp32.  As operands the
-// weighted C goes in three planes (exact), state and scores in three where
-// the outputs are fp32 or feed the decays' gradient, in two where they are
-// rounded to bf16 anyway (2^-17 against the outputs' 2^-8; one plane would
-// add an error as large as the outputs' own).
+// weighted C goes in three planes (all 24 bits), state and scores in three
+// where the outputs are fp32, and in all three walks of the gradients (dq and
+// dk feed the decays' gradient; dv, which does not, is walked by the same
+// kernel); in two where a forward's outputs are rounded to bf16 anyway (2^-17
+// against the outputs' 2^-8; one plane would add an error as large as the
+// outputs' own).
 //
-// What bounds it (64 tokens x 128 x 128, bf16): 800 matrix-core instructions
-// of 16 cycles, 4300 vector and 900 LDS ones per chunk.  With every compute
-// unit busy a chunk takes about 10,000 cycles at one or at two workgroups per
-// unit, of which some instruction issues in 85%, vector ALU 58%, LDS 47%,
-// matrix cores 36%, and the clock falls to 1.9 GHz: it is bound by its
-// instructions, not by latency (doubling the LDS buffers, reading operands a
-// step ahead and loading two chunks ahead each changed nothing) nor by memory
-// (2 to 3 TB/s).  Measured: 4096 tokens x 32 heads in segments of 512, 49 us
-// (fold 25, scan 7).
+// What bounds it (64 tokens x 128 x 128, bf16): 776 matrix-core instructions
+// of 16 cycles, 4300 vector and 770 LDS ones per chunk.  With every compute
+// unit busy (16 packed sequences, 32 heads, one workgroup per unit) a chunk
+// takes about 9,600 cycles, of which the vector ALU is busy 47%, the matrix
+// cores 32%, the LDS 42% (a third of that in bank conflicts), and some
+// instruction issues in 67%; with three walks and two workgroups per unit (the
+// gradients) 55%, 33%, 40% and 80%.  So neither unit is at its limit: vector
+// and matrix work hardly overlap, as all waves of a workgroup pass the same
+// phase between two barriers, and the phases are fenced from each other.
+// Doubling the LDS buffers, reading operands a step ahead and loading two
+// chunks ahead each changed nothing; memory is far from its limit (2 to 3
+// TB/s).  Measured: 4096 tokens x 32 heads in segments of 512, 49 us (fold 25,
+// scan 7).
 template <int KIND, int NPO, typename TI, typename TO>
 __global__ __launch_bounds__(64 * LIN_NW, lin_waves<TI>()) void linear_kernel(LinArgs p) {
   constexpr bool FOLD = KIND == LIN_FOLD, GRAD = KIND == LIN_GRAD;
@@ -375,7 +384,8 @@ __global__ __launch_bounds__(64 * LIN_NW, lin_waves<TI>()) void linear_kernel(Li
   // Where piece c of row r lies: its index is XORed with the row's, the row's
   // two low bits above its next two.  16 consecutive rows' pieces of one index
   // are then in 16 different places (row reads), and so are 4 aligned pieces of
-  // 4 aligned rows (transposing reads): no bank conflicts in either.
+  // 4 aligned rows (transposing reads).  Without it the conflicts took 80
+  // million cycles of a packed call, with it 48 million of the LDS's 137.
   auto piece_of = [&](int r, int c) __attribute__((always_inline)) -> int {
     return r * D + ((c ^ ((r & 3) << 2 | (r >> 2 & 3))) << 3);
   };

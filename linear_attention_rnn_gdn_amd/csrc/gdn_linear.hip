@@ -27,6 +27,21 @@ namespace {
 //   gradients, 4096 x 32              430 / 312 / 250 / 228 / 252 / 329
 //   gradients, 8192 x 4               115 /  89 /  86 / 103 / 163 / 294
 //   gradients, 2048 x 8                68 /  59 /  65 /  97 / 160 / 228
+// and fp32, 64 / 128 / 256 / 512 (the rule's):
+//   forward, 509 x 2                   29 /  40 /  63 /  67 (64)
+//   forward, 2 x 1001 x 4              37 /  44 /  64 / 110 (64)
+//   forward, 8192 x 4                  68 /  58 /  71 / 113 (128)
+//   forward, 4096 x 32                221 / 162 / 139 / 138 (512)
+//   gradients, 509 x 2                 34 /  46 /  71 /  83 (64)
+//   gradients, 2 x 1001 x 4            58 /  56 /  79 / 129 (64)
+//   gradients, 8192 x 4               170 / 138 / 140 / 153 (128)
+//   gradients, 4096 x 32              645 / 517 / 448 / 413 (512)
+// Known to be slow: forwards whose (row, value head) pairs number 129 to 255.
+// Each sequence is then cut into a long and a short segment, and the fold of the
+// long one comes before the walks.  Measured, 4096 tokens x 32 heads, this rule /
+// two even segments / one: 5 rows 383 / 325 / 268, 6 rows 462 / 336 / 272, 7 rows
+// 536 / 365 / 294, 6 rows fp32 924 / 672 / 537 (4 rows, where the rule's two are
+// even: 237, one 265).  The gradients hardly differ: 6 rows 1165 / 1165 / 1162.
 constexpr int kWalks = 256, kMaxGradSegment = 2048, kFewWalks = 4 * kWalks, kShort = 256, kLdsToBeAlone = 24 << 10;
 
 struct Plan {

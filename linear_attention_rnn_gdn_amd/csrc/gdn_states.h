@@ -48,9 +48,12 @@ __device__ __forceinline__ float4 ld_state(const float *p) { return *reinterpret
 // RPT rows of a state, D floats apart.  `stream`: past the caches, for calls
 // that write more state than the memory-side cache (256 MB) keeps; a smaller
 // pool's states are still there for the next step and are stored plainly.
-// Measured with 32 value heads: 256 rows (512 MB of state) streamed / plain
-// 183 / 190 us a step, 171 / 199 us a commit; 32 rows of a pool of 256 MB
-// 23.4 / 22.2 and 26.5 / 23.6 us.
+// Measured with 32 value heads on a pool of as many slots as rows, the same
+// call again and again, streamed / plain, us a step and a commit of 6 nodes:
+//    32 rows   64 MB   23 /  23    26 /  25      144 rows  288 MB   91 /  95    96 / 103
+//    96 rows  192 MB   62 /  62    67 /  65      160 rows  320 MB  102 / 116   107 / 124
+//   112 rows  224 MB   71 /  71    78 /  75      192 rows  384 MB  135 / 156   127 / 166
+//   128 rows  256 MB   80 /  83    87 /  90      256 rows  512 MB  212 / 213   175 / 221
 template <int RPT>
 __device__ __forceinline__ void st_state(float *p, const float4 (&x)[RPT], bool stream) {
   if (stream) {
@@ -310,8 +313,8 @@ __global__ __launch_bounds__(256) void tree_commit_kernel(StateArgs a) {
 template <typename TI> struct TreePitch { static constexpr int v = D + 8; };   // elements of K, Q rows in LDS
 template <> struct TreePitch<float> { static constexpr int v = D + 4; };
 
-// workgroups per compute unit: two, but for the largest fp32 trees, whose rows
-// fill more than half of the LDS
+// workgroups per compute unit: two, but for the largest fp32 trees, which take
+// more than half of the LDS (86 or 109 of 160 KB)
 template <int MT, typename TI> constexpr int tree_wgs() { return MT == 4 && std::is_same<TI, float>::value ? 1 : 2; }
 
 template <int MT, int NT, typename TI, typename TO, bool DELTA>
