@@ -484,6 +484,165 @@ gdn_status gdn_linear_chunk_bwd(const gdn_linear_shape *shape, const void *q, co
                                 const float *dh_T, void *dq, void *dk, void *dv, float *dg,
                                 float *dh0, void *ws, size_t ws_bytes, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The short causal convolution in front of a recurrent layer: one filter of W
+ * taps per channel, over time,
+ *     pre[t, c] = bias[c] + sum_w weight[c, w] x[t - (W - 1) + w, c],
+ *     y = pre sigmoid(pre) (silu = 1), or pre.
+ * Tokens before a sequence's first are the rows of its window: the last W - 1
+ * tokens of what came before, oldest first, or zero.
+ *   B        rows (packed: sequences)
+ *   T        tokens per row (packed: in all; gdn_conv_step: 1)
+ *   C, W     channels, taps (2, 3 or 4)
+ *   ld       elements from a token of x to the next (0: C): x may be columns of
+ *            a wider tensor, all its B * T tokens evenly spaced
+ *   n_slots  gdn_conv_step: slots of the pool
+ *   silu     1: the activation above
+ *   dtype    of x, y, windows, dy, dx, dh0, dh_T; weight, bias and their
+ *            gradients are fp32
+ * Pointers have to be aligned to an element only; rows that are whole 16-byte
+ * pieces (C and ld multiples of 16 bytes, pointers 16-byte aligned) are faster.
+ * Sums are fp32, rounded once.  C <= 2^24, T <= 2^30, and a launch has to stay
+ * below 2^32 threads (GDN_ERR_SHAPE). */
+typedef struct {
+  int32_t B, T, C, W, ld, n_slots, silu, dtype;
+} gdn_conv_shape;
+
+/*   x [B, T, C]; weight [C, W]; bias [C] or NULL; h0 [B, W - 1, C] windows, NULL
+ *   = zero; y [B, T, C] (written); h_T [B, W - 1, C] the windows behind the
+ *   last tokens, NULL = not wanted (written).  Outputs must not overlap inputs. */
+gdn_status gdn_conv_fwd(const gdn_conv_shape *shape, const void *x, const float *weight,
+                        const float *bias, const void *h0, void *y, void *h_T, void *hip_stream);
+
+/* Packed sequences: x, y [T, C]; cu_seqlens [B + 1] int32 DEVICE array, a
+ * partition of [0, T] (for other offsets the results are unspecified, but
+ * nothing outside the tensors is touched); an empty sequence's h_T is its h0. */
+gdn_status gdn_conv_fwd_varlen(const gdn_conv_shape *shape, const int32_t *cu_seqlens, const void *x,
+                               const float *weight, const float *bias, const void *h0, void *y,
+                               void *h_T, void *hip_stream);
+
+/* One token of every row: x, y [B, C]; state [n_slots, W - 1, C] windows, moved
+ * on in place; slots [B] int32 or NULL as for the pool of recurrent states (a
+ * row whose slot is outside the pool, or is an earlier row's, gets a zero
+ * output and writes no window). */
+gdn_status gdn_conv_step(const gdn_conv_shape *shape, const void *x, const float *weight,
+                         const float *bias, const int32_t *slots, void *state, void *y,
+                         void *hip_stream);
+
+/* The gradients of L = sum <y, dy> + <h_T, dh_T>: dx [B, T, C], dweight [C, W],
+ * dbias [C] or NULL, dh0 [B, W - 1, C] or NULL (of h0, also where h0 is NULL:
+ * zero windows).  dh_T NULL = zero.  Sums over tokens are made in a fixed order. */
+gdn_status gdn_workspace_size_conv_bwd(const gdn_conv_shape *shape, size_t *bytes);
+gdn_status gdn_conv_bwd(const gdn_conv_shape *shape, const void *x, const float *weight,
+                        const float *bias, const void *h0, const void *dy, const void *dh_T, void *dx,
+                        float *dweight, float *dbias, void *dh0, void *ws, size_t ws_bytes,
+                        void *hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * The selective state space scan.  Per channel c, with N states h_n:
+ *     d = softplus(dt + dt_bias)  (softplus = 0: dt + dt_bias),
+ *     h_n <- exp(d A[c, n]) h_n + d x B_n,
+ *     s = sum_n C_n h_n + D[c] x,    y = s z sigmoid(z)  (z NULL: s).
+ * B and C belong to a token and a group of C / G neighbouring channels.
+ *   B        rows (packed: sequences)
+ *   T        tokens per row (packed: in all; gdn_ssm_step: 1)
+ *   C, N, G  channels, states per channel (8, 16 or 32), groups
+ *   n_slots  gdn_ssm_step: slots of the pool
+ *   softplus 0 or 1
+ *   ld_x, ld_dt, ld_z, ld_b, ld_c   elements from a token of x, dt, z, B, C to
+ *            the next (0: dense), so that they may be columns of wider tensors;
+ *            ld_b and ld_c times the element a multiple of 16 bytes
+ *   dtype    of x, dt, z, B, C and, in the gradients, dy and theirs
+ *   o_dtype  of y
+ * A, D, dt_bias and their gradients, and the states, are fp32.  x, dt, z, dy,
+ * dx, ddt and dz are aligned to an element, all else to 16 bytes (D, dt_bias, slots and
+ * offsets: 4).  T <= 2^30, C <= 2^20, and launches stay below 2^31 threads
+ * (GDN_ERR_SHAPE).  Outputs must not overlap inputs or each other. */
+typedef struct {
+  int32_t B, T, C, N, G, n_slots, softplus;
+  int32_t ld_x, ld_dt, ld_z, ld_b, ld_c;
+  int32_t dtype, o_dtype;
+} gdn_ssm_shape;
+
+/* x, dt, z [B, T, C] (z NULL: no gate); B, C [B, T, G, N]; A [C, N]; D, dt_bias
+ * [C] or NULL (none). */
+typedef struct {
+  const void *x, *dt, *z, *B, *C;
+  const float *A, *D, *dt_bias;
+} gdn_ssm_inputs;
+
+/* dx, ddt, dz as x, dt, z, but dense; dB, dC dense [B, T, G, N]; dA [C, N]; dD,
+ * ddt_bias [C] or NULL; dh0 [B, C, N] or NULL. */
+typedef struct {
+  void *dx, *ddt, *dz, *dB, *dC;
+  float *dA, *dD, *ddt_bias, *dh0;
+} gdn_ssm_grads;
+
+#define GDN_SSM_FWD 0
+#define GDN_SSM_VARLEN 1
+#define GDN_SSM_BWD 2
+gdn_status gdn_workspace_size_ssm(const gdn_ssm_shape *shape, int32_t kind, size_t *bytes);
+
+/* h0 [B, C, N] initial states, NULL = zero; y [B, T, C] (written); h_T [B, C, N]
+ * final states, NULL = not wanted (written). */
+gdn_status gdn_ssm_fwd(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, const float *h0, void *y,
+                       float *h_T, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* Packed sequences (the tokens of all of them one row; cu_seqlens as for
+ * gdn_conv_fwd_varlen).  An empty sequence's h_T is its h0. */
+gdn_status gdn_ssm_fwd_varlen(const gdn_ssm_shape *shape, const int32_t *cu_seqlens,
+                              const gdn_ssm_inputs *in, const float *h0, void *y, float *h_T, void *ws,
+                              size_t ws_bytes, void *hip_stream);
+
+/* One token of every row (inputs without the T dimension): state [n_slots, C, N]
+ * advanced in place, slots as for gdn_conv_step. */
+gdn_status gdn_ssm_step(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, const int32_t *slots,
+                        float *state, void *y, void *hip_stream);
+
+/* The gradients of L = sum <y, dy> + <h_T, dh_T>: dy [B, T, C] dtype; dh_T
+ * [B, C, N] fp32 or NULL (zero); o_dtype is not used.  Sums over tokens and
+ * channels are made in a fixed order. */
+gdn_status gdn_ssm_bwd(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, const float *h0,
+                       const void *dy, const float *dh_T, const gdn_ssm_grads *out, void *ws,
+                       size_t ws_bytes, void *hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers: between gdn_tree_fwd, whose outputs lead to the target's
+ * probabilities, and gdn_tree_commit, which takes `last`.  A row's tree is
+ * walked from the root (-1).  With p the target's probabilities behind the node
+ * reached, its children (the nodes r with that parent) are looked at in order:
+ *   draft NULL (tokens chosen without chance): accepted if
+ *     uniform[r] (1 - sum of the refused siblings' p) < p(tokens[r]), and a
+ *     refused child's token is taken out of p;
+ *   draft given (siblings drawn from q, the draft's probabilities behind their
+ *     parent): accepted if uniform[r] q(x) < p(x); a refusal leaves
+ *     max(p - q, 0), scaled to one (if it has no mass, p stays).
+ * The walk goes on from the first child accepted.  Where there is none, the next
+ * token is the lowest v at which the running sum of what is left of p passes
+ * uniform[n] times its whole; -1 if p has no mass.  The tokens accepted, and
+ * that one, are distributed as the target's.
+ *   B, n, V  rows, nodes per row (1..64), tokens of the vocabulary (<= 2^24)
+ *   tokens, parents [B, n] int32: a node's token and its parent, an earlier
+ *            node or -1; a node with another parent, or a token outside
+ *            [0, V), is absent (so are its descendants)
+ *   target   [B, n + 1, V] fp32: row 0 behind the root, row r + 1 behind node r
+ *   draft    [B, n, V] fp32 or NULL: the same rows (that of node n - 1, which
+ *            has no children, is left out)
+ *   uniform  [B, n + 1] fp32 in [0, 1): one per node, the last for the token
+ *   last     [B] the last node accepted, -1: none; token [B] the next token;
+ *   path     [B, n] the nodes accepted, in order, then -1 (all int32, written)
+ * Rows of target and draft that the walk does not reach are not read, but for
+ * single values.  Weights that are negative or no numbers count as zero.  Sums
+ * and comparisons are fp64.  B <= 2^20, B * ceil(V / 4096) <= 2^23. */
+typedef struct {
+  int32_t B, n, V;
+} gdn_verify_shape;
+gdn_status gdn_workspace_size_verify(const gdn_verify_shape *shape, size_t *bytes);
+gdn_status gdn_tree_verify(const gdn_verify_shape *shape, const int32_t *tokens, const int32_t *parents,
+                           const float *target, const float *draft, const float *uniform, int32_t *last,
+                           int32_t *token, int32_t *path, void *ws, size_t ws_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

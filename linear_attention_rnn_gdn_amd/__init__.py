@@ -20,6 +20,18 @@ States in a pool [n_slots,H_v,d_k,d_v], for serving (beta=None: the linear rule)
   step(q, k, v, g, beta, state, slots=None)                     -> o
   tree_fwd(q, k, v, g, beta, parents, state, slots=None)        -> (o, u)
   tree_commit(k, u, g, parents, last, state, slots=None)        -> state
+What stands around such a layer.  The short causal convolution:
+  conv_fwd(x, weight, bias=None, h0=None, activation="silu")    -> (y, h_T)
+  conv_fwd_varlen(x, weight, cu_seqlens, bias=None, h0=None)    -> (y, h_T)
+  conv_bwd(x, weight, dy, bias=None, h0=None, dh_T=None)        -> gradients
+  conv_step(x, weight, state, bias=None, slots=None)            -> y
+The selective state space scan (8, 16 or 32 states per channel):
+  ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None) -> (y, h_T)
+  ssm_fwd_varlen(x, dt, A, B, C, cu_seqlens, ...)               -> (y, h_T)
+  ssm_bwd(x, dt, A, B, C, dy, ...)                              -> gradients
+  ssm_step(x, dt, A, B, C, state, ..., slots=None)              -> y
+The verification of drafted tokens, between tree_fwd and tree_commit:
+  tree_verify(tokens, parents, target, uniform, draft=None)     -> (last, token, path)
 Outputs and a workspace that a caller passes to these (out, final_state,
 values, workspace) are refused where they overlap an input or each other.
 """
@@ -56,6 +68,27 @@ class GdnLinearShape(ctypes.Structure):
                 ("B", "T", "H_qk", "H_v", "d_k", "d_v", "g_fixed", "dtype", "o_dtype")]
 
 
+class GdnConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "C", "W", "ld", "n_slots", "silu", "dtype")]
+
+
+class GdnSsmShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "T", "C", "N", "G", "n_slots", "softplus", "ld_x", "ld_dt", "ld_z", "ld_b", "ld_c", "dtype", "o_dtype")]
+
+
+class GdnSsmInputs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias")]
+
+
+class GdnSsmGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")]
+
+
+class GdnVerifyShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "n", "V")]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS.get(status, status)} (status {status})")
@@ -70,7 +103,10 @@ SYMBOLS = ("gdn_status_str", "gdn_validate", "gdn_workspace_size", "gdn_workspac
            "gdn_chunk_transform", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_affine",
            "gdn_workspace_size_bwd", "gdn_chunk_bwd_state", "gdn_workspace_size_bwd_grads", "gdn_chunk_bwd",
            "gdn_step", "gdn_tree_fwd", "gdn_tree_commit", "gdn_workspace_size_linear", "gdn_linear_chunk_fwd",
-           "gdn_linear_chunk_fwd_varlen", "gdn_linear_chunk_bwd")
+           "gdn_linear_chunk_fwd_varlen", "gdn_linear_chunk_bwd",
+           "gdn_conv_fwd", "gdn_conv_fwd_varlen", "gdn_conv_step", "gdn_workspace_size_conv_bwd", "gdn_conv_bwd",
+           "gdn_workspace_size_ssm", "gdn_ssm_fwd", "gdn_ssm_fwd_varlen", "gdn_ssm_step", "gdn_ssm_bwd",
+           "gdn_workspace_size_verify", "gdn_tree_verify")
 STAGE_PREP, STAGE_FOLD, STAGE_PREFIX, STAGE_WALK, STAGE_OUT, STAGE_ALL = 1, 2, 4, 8, 16, 31
 
 
@@ -134,6 +170,18 @@ def lib():
         L.gdn_linear_chunk_fwd_varlen.restype = I
         L.gdn_linear_chunk_bwd.argtypes = [LP] + [P] * 13 + [SZ, P]
         L.gdn_linear_chunk_bwd.restype = I
+        CP, MP, VP = (ctypes.POINTER(t) for t in (GdnConvShape, GdnSsmShape, GdnVerifyShape))
+        IP, GP = ctypes.POINTER(GdnSsmInputs), ctypes.POINTER(GdnSsmGrads)
+        for name, args in (("gdn_conv_fwd", [CP] + [P] * 7), ("gdn_conv_fwd_varlen", [CP] + [P] * 8),
+                           ("gdn_conv_step", [CP] + [P] * 7), ("gdn_workspace_size_conv_bwd", [CP, ctypes.POINTER(SZ)]),
+                           ("gdn_conv_bwd", [CP] + [P] * 11 + [SZ, P]),
+                           ("gdn_workspace_size_ssm", [MP, I, ctypes.POINTER(SZ)]),
+                           ("gdn_ssm_fwd", [MP, IP] + [P] * 4 + [SZ, P]), ("gdn_ssm_fwd_varlen", [MP, P, IP] + [P] * 4 + [SZ, P]),
+                           ("gdn_ssm_step", [MP, IP] + [P] * 4), ("gdn_ssm_bwd", [MP, IP] + [P] * 3 + [GP, P, SZ, P]),
+                           ("gdn_workspace_size_verify", [VP, ctypes.POINTER(SZ)]),
+                           ("gdn_tree_verify", [VP] + [P] * 9 + [SZ, P])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = I
         _lib = L
     return _lib
 
@@ -525,11 +573,13 @@ def _addr(t):
 def _check_apart(outputs, inputs):
     """Outputs (and a workspace) that the caller passed must lie apart from
     the inputs and from each other: workgroups that still read an input run
-    beside those that write.  Both are (tensor or None, name) pairs of
-    contiguous tensors."""
+    beside those that write.  Both are (tensor or None, name) pairs; of a
+    tensor that is not contiguous the whole range from its first to its last
+    element counts."""
     def span(t, name):
         at = t.data_ptr()
-        return at, at + t.numel() * t.element_size(), name
+        n = t.numel() if t.is_contiguous() else 1 + sum((k - 1) * m for k, m in zip(t.shape, t.stride()))
+        return at, at + n * t.element_size(), name
 
     taken = [span(t, name) for t, name in inputs if t is not None and t.numel()]
     for t, name in outputs:
@@ -782,3 +832,388 @@ def linear_chunk_bwd(q, k, v, g, dO, h0=None, dh_T=None, workspace=None, out=Non
                                           _addr(out["dg"]), _addr(out["dh0"]), _addr(ws), ws.numel(), st),
                "gdn_linear_chunk_bwd")
     return out
+
+
+# ---------------------------------------------------------------------------
+# around a recurrent layer: the short convolution, the selective scan
+
+
+def _columns(t, name, dtype, shape, dev, tail):
+    """Checks a tensor that may be columns of a wider one: the last ``tail``
+    dimensions dense, the tokens before them evenly spaced.  Returns the
+    elements from a token to the next (0: dense)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return 0
+    strides, width = t.stride(), 1
+    for i in range(len(shape) - 1, len(shape) - 1 - tail, -1):
+        if shape[i] > 1 and strides[i] != width:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        width *= shape[i]
+    ld = None
+    for i in range(len(shape) - 1 - tail, -1, -1):
+        if shape[i] == 1:
+            continue
+        if ld is None:
+            ld = after = strides[i]
+        elif strides[i] != after:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+        after *= shape[i]
+    if ld is None:
+        return 0
+    if not width <= ld < 1 << 31:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return ld
+
+
+def _leading(t, name, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    return t.shape
+
+
+def _device_offsets(x, cu_seqlens, stream):
+    """Packed sequences' offsets on the device, and how many sequences."""
+    if x.shape[0] != 1:
+        raise ValueError("packed sequences: the batch dimension must be 1")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    if not isinstance(cu_seqlens, torch.Tensor):
+        with _on(x.device, stream):   # (on the call's stream, as in linear_chunk_fwd_varlen)
+            cu_seqlens = torch.tensor(list(cu_seqlens), dtype=torch.int32, device=x.device)
+    n = cu_seqlens.numel() - 1
+    if n < 1:
+        raise ValueError("cu_seqlens must hold at least two offsets")
+    _check_tensors(x.device, (cu_seqlens, "cu_seqlens", torch.int32, (n + 1,)))
+    return cu_seqlens, n
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_plan(grads, *sizes):
+    """(shape, workspace bytes) of a call's sizes."""
+    shape = GdnConvShape(*sizes)
+    n = ctypes.c_size_t(0)
+    if grads:
+        _check(lib().gdn_workspace_size_conv_bwd(shape, ctypes.byref(n)), "gdn_workspace_size_conv_bwd")
+    return shape, int(n.value)
+
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _activation(name):
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _conv_inputs(x, weight, bias, dims):
+    """Checks x, weight and bias; returns the token stride, C and W."""
+    xs = _leading(x, "x", dims)
+    _dt(x.dtype)
+    C, W = _leading(weight, "weight", 2)
+    ld = _columns(x, "x", x.dtype, xs[:-1] + (C,), x.device, 1)
+    _check_tensors(x.device, (weight, "weight", torch.float32, (C, W)))
+    if bias is not None:
+        _check_tensors(x.device, (bias, "bias", torch.float32, (C,)))
+    return ld, C, W
+
+
+def _conv_fwd(rows, cu, x, weight, bias, h0, activation, output_final_state, out, final_state, stream):
+    ld, C, W = _conv_inputs(x, weight, bias, 3)
+    silu, dev, (B, T, _) = _activation(activation), x.device, x.shape
+    n = B if rows is None else rows
+    window = (n, W - 1, C)
+    for t, name, shape in ((h0, "h0", window), (out, "y", (B, T, C)), (final_state, "h_T", window)):
+        if t is not None:
+            _check_tensors(dev, (t, name, x.dtype, shape))
+    if not (out is None and final_state is None):
+        _check_apart(((out, "y"), (final_state, "h_T")),
+                     ((x, "x"), (weight, "weight"), (bias, "bias"), (h0, "h0"), (cu, "cu_seqlens")))
+    shape, _ = _conv_plan(False, n, T, C, W, ld, 0, silu, _dt(x.dtype))
+    with _on(dev, stream) as st:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=dev) if out is None else out
+        hT = None
+        if output_final_state:
+            hT = torch.empty(window, dtype=x.dtype, device=dev) if final_state is None else final_state
+        args = (_addr(x), _addr(weight), _addr(bias), _addr(h0), _addr(y), _addr(hT), st)
+        if rows is None:
+            _check(lib().gdn_conv_fwd(shape, *args), "gdn_conv_fwd")
+        else:
+            _check(lib().gdn_conv_fwd_varlen(shape, _addr(cu), *args), "gdn_conv_fwd_varlen")
+    return y, hT
+
+
+def conv_fwd(x, weight, bias=None, h0=None, activation="silu", output_final_state=True, out=None, final_state=None,
+             stream=None):
+    """The short causal convolution (gdn_conv_fwd): y[t] = act(bias + sum_w
+    weight[:, w] x[t - (W - 1) + w]), one filter per channel.
+
+    x [B,T,C] (bf16 or fp32; it may be columns of a wider tensor); weight [C,W]
+    fp32, W 2 to 4; bias [C] fp32 or None; h0 [B,W-1,C] in x's dtype: the tokens
+    before the first, oldest first (None: zeros); activation "silu" or None.
+    Returns (y [B,T,C] in x's dtype, h_T [B,W-1,C], the last W - 1 tokens, or
+    None)."""
+    return _conv_fwd(None, None, x, weight, bias, h0, activation, output_final_state, out, final_state, stream)
+
+
+def conv_fwd_varlen(x, weight, cu_seqlens, bias=None, h0=None, activation="silu", output_final_state=True, out=None,
+                    final_state=None, stream=None):
+    """conv_fwd over packed sequences (gdn_conv_fwd_varlen): x [1,T,C];
+    cu_seqlens as in chunk_fwd_varlen; h0 and h_T [n,W-1,C]."""
+    _leading(x, "x", 3)
+    cu_seqlens, n = _device_offsets(x, cu_seqlens, stream)
+    return _conv_fwd(n, cu_seqlens, x, weight, bias, h0, activation, output_final_state, out, final_state, stream)
+
+
+def conv_bwd(x, weight, dy, bias=None, h0=None, dh_T=None, activation="silu", workspace=None, out=None, stream=None):
+    """Gradients of sum <y, dy> + <h_T, dh_T> through conv_fwd (gdn_conv_bwd).
+    dy [B,T,C] and dh_T [B,W-1,C] (or None) in x's dtype.  Returns a dict
+    (``out``: such a dict to write into): dx [B,T,C] and dh0 [B,W-1,C] in x's
+    dtype, dweight [C,W] and, with a bias, dbias [C] fp32."""
+    ld, C, W = _conv_inputs(x, weight, bias, 3)
+    silu, dev, dt, (B, T, _) = _activation(activation), x.device, x.dtype, x.shape
+    window = (B, W - 1, C)
+    _check_tensors(dev, (dy, "dy", dt, (B, T, C)))
+    for t, name in ((h0, "h0"), (dh_T, "dh_T")):
+        if t is not None:
+            _check_tensors(dev, (t, name, dt, window))
+    want = dict(dx=(dt, (B, T, C)), dweight=(torch.float32, (C, W)), dh0=(dt, window))
+    if bias is not None:
+        want["dbias"] = (torch.float32, (C,))
+    shape, need = _conv_plan(True, B, T, C, W, ld, 0, silu, _dt(dt))
+    inputs = ((x, "x"), (weight, "weight"), (bias, "bias"), (h0, "h0"), (dy, "dy"), (dh_T, "dh_T"))
+    _check_grads(want, out, workspace, inputs, dev)
+    with _on(dev, stream) as st:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if out is None:
+            out = {name: torch.empty(sh, dtype=t, device=dev) for name, (t, sh) in want.items()}
+        _check(lib().gdn_conv_bwd(shape, _addr(x), _addr(weight), _addr(bias), _addr(h0), _addr(dy), _addr(dh_T),
+                                  _addr(out["dx"]), _addr(out["dweight"]), _addr(out["dbias"]) if bias is not None else None,
+                                  _addr(out["dh0"]), _addr(ws), ws.numel(), st), "gdn_conv_bwd")
+    return out
+
+
+def _check_grads(want, out, workspace, inputs, dev):
+    """The outputs and the workspace of a gradient call that the caller passed."""
+    if out is not None:
+        for name, (dt, sh) in want.items():
+            _check_tensors(dev, (out[name], name, dt, sh))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    if not (out is None and workspace is None):
+        _check_apart([(out[name], name) for name in want if out is not None] + [(workspace, "workspace")], inputs)
+
+
+def conv_step(x, weight, state, bias=None, slots=None, activation="silu", out=None, stream=None):
+    """One token of every row (gdn_conv_step), for decoding: x [B,C]; state
+    [n_slots,W-1,C] in x's dtype, a pool of windows moved on in place; slots as
+    in step.  A row without a slot, or with an earlier row's, gets a zero output
+    and writes no window.  Returns y [B,C]."""
+    ld, C, W = _conv_inputs(x, weight, bias, 2)
+    silu, dev, dt, B = _activation(activation), x.device, x.dtype, x.shape[0]
+    n_slots = _leading(state, "state", 3)[0]
+    _check_tensors(dev, (state, "state", dt, (n_slots, W - 1, C)))
+    if slots is not None:
+        _check_tensors(dev, (slots, "slots", torch.int32, (B,)))
+    if out is not None:
+        _check_tensors(dev, (out, "y", dt, (B, C)))
+        _check_apart(((out, "y"),), ((x, "x"), (weight, "weight"), (bias, "bias"), (state, "state"), (slots, "slots")))
+    shape, _ = _conv_plan(False, B, 1, C, W, ld, n_slots, silu, _dt(dt))
+    with _on(dev, stream) as st:
+        y = torch.empty((B, C), dtype=dt, device=dev) if out is None else out
+        _check(lib().gdn_conv_step(shape, _addr(x), _addr(weight), _addr(bias), _addr(slots), _addr(state), _addr(y), st),
+               "gdn_conv_step")
+    return y
+
+
+SSM_FWD, SSM_VARLEN, SSM_BWD = 0, 1, 2
+
+
+@functools.lru_cache(maxsize=256)
+def _ssm_plan(kind, *sizes):
+    """(shape, workspace bytes) of a call's sizes; kind None: a step."""
+    shape = GdnSsmShape(*sizes)
+    n = ctypes.c_size_t(0)
+    if kind is not None:
+        _check(lib().gdn_workspace_size_ssm(shape, kind, ctypes.byref(n)), "gdn_workspace_size_ssm")
+    return shape, int(n.value)
+
+
+def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, lead):
+    """Checks the inputs of a scan or a step; returns its sizes (channels,
+    states, groups) and token strides, the C struct and the inputs' names."""
+    xs = _leading(x, "x", lead + 1)
+    _dt(x.dtype)
+    dev, ty, c = x.device, x.dtype, xs[-1]
+    n = _leading(A, "A", 2)[1]
+    g = _leading(B, "B", lead + 2)[-2]
+    lds = [_columns(x, "x", ty, xs, dev, 1), _columns(dt, "dt", ty, xs, dev, 1),
+           0 if z is None else _columns(z, "z", ty, xs, dev, 1)]
+    lds += [_columns(t, name, ty, xs[:-1] + (g, n), dev, 2) for t, name in ((B, "B"), (C, "C"))]
+    _check_tensors(dev, (A, "A", torch.float32, (c, n)))
+    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _check_tensors(dev, (t, name, torch.float32, (c,)))
+    given = GdnSsmInputs(_addr(x), _addr(dt), _addr(z), _addr(B), _addr(C), _addr(A), _addr(D), _addr(dt_bias))
+    named = [(x, "x"), (dt, "dt"), (z, "z"), (B, "B"), (C, "C"), (A, "A"), (D, "D"), (dt_bias, "dt_bias")]
+    return (c, n, g), lds, given, named
+
+
+def _ssm_fwd(rows, cu, x, dt, A, B, C, D, z, dt_bias, h0, softplus, o_dtype, output_final_state, workspace, out,
+             final_state, stream):
+    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2)
+    dev, (b, T, _) = x.device, x.shape
+    seqs = b if rows is None else rows
+    state = (seqs, c, n)
+    for t, name, ty, sh in ((h0, "h0", torch.float32, state), (out, "y", o_dtype, (b, T, c)), (final_state, "h_T", torch.float32, state)):
+        if t is not None:
+            _check_tensors(dev, (t, name, ty, sh))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    if not (out is None and final_state is None and workspace is None):
+        _check_apart(((out, "y"), (final_state, "h_T"), (workspace, "workspace")), named + [(h0, "h0"), (cu, "cu_seqlens")])
+    shape, need = _ssm_plan(SSM_FWD if rows is None else SSM_VARLEN, seqs, T, c, n, g, 0, int(bool(softplus)), *lds,
+                            _dt(x.dtype), _dt(o_dtype))
+    with _on(dev, stream) as st:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        y = torch.empty((b, T, c), dtype=o_dtype, device=dev) if out is None else out
+        hT = None
+        if output_final_state:
+            hT = torch.empty(state, dtype=torch.float32, device=dev) if final_state is None else final_state
+        args = (given, _addr(h0), _addr(y), _addr(hT), _addr(ws), ws.numel(), st)
+        if rows is None:
+            _check(lib().gdn_ssm_fwd(shape, *args), "gdn_ssm_fwd")
+        else:
+            _check(lib().gdn_ssm_fwd_varlen(shape, _addr(cu), *args), "gdn_ssm_fwd_varlen")
+    return y, hT
+
+
+def ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, softplus=True, o_dtype=torch.float32,
+            output_final_state=True, workspace=None, out=None, final_state=None, stream=None):
+    """The selective state space scan (gdn_ssm_fwd).  Per channel, with N
+    states: d = softplus(dt + dt_bias) (``softplus`` false: dt + dt_bias),
+    h = exp(d A) h + d x B, y = (<C, h> + D x) silu(z).
+
+    x, dt, z [B,T,c] and B, C [B,T,G,N] (bf16 or fp32, one dtype; each may be
+    columns of a wider tensor); A [c,N], D and dt_bias [c] fp32; N 8, 16 or 32;
+    G groups of neighbouring channels; z, D and dt_bias may be None; h0 [B,c,N]
+    fp32 or None.  Returns (y [B,T,c] o_dtype, h_T [B,c,N] fp32 or None)."""
+    return _ssm_fwd(None, None, x, dt, A, B, C, D, z, dt_bias, h0, softplus, o_dtype, output_final_state, workspace, out,
+                    final_state, stream)
+
+
+def ssm_fwd_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, h0=None, softplus=True,
+                   o_dtype=torch.float32, output_final_state=True, workspace=None, out=None, final_state=None, stream=None):
+    """ssm_fwd over packed sequences (gdn_ssm_fwd_varlen): the batch dimension
+    is 1; cu_seqlens as in chunk_fwd_varlen; h0 and h_T [n,c,N]."""
+    _leading(x, "x", 3)
+    cu_seqlens, n = _device_offsets(x, cu_seqlens, stream)
+    return _ssm_fwd(n, cu_seqlens, x, dt, A, B, C, D, z, dt_bias, h0, softplus, o_dtype, output_final_state, workspace, out,
+                    final_state, stream)
+
+
+def ssm_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None, dh_T=None, softplus=True, workspace=None, out=None,
+            stream=None):
+    """Gradients of sum <y, dy> + <h_T, dh_T> through ssm_fwd (gdn_ssm_bwd).
+    dy [B,T,c] in x's dtype; h0, dh_T [B,c,N] fp32 or None.  Returns a dict
+    (``out``: such a dict to write into): dx, ddt, dB, dC and, with z, dz in x's
+    dtype; dA, dh0 and, where given, dD and ddt_bias fp32."""
+    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2)
+    dev, ty, (b, T, _) = x.device, x.dtype, x.shape
+    f32, row, state = torch.float32, (b, T, c), (b, c, n)
+    _check_tensors(dev, (dy, "dy", ty, row))
+    for t, name in ((h0, "h0"), (dh_T, "dh_T")):
+        if t is not None:
+            _check_tensors(dev, (t, name, f32, state))
+    want = dict(dx=(ty, row), ddt=(ty, row), dB=(ty, (b, T, g, n)), dC=(ty, (b, T, g, n)), dA=(f32, (c, n)), dh0=(f32, state))
+    for name, t, what in (("dz", z, (ty, row)), ("dD", D, (f32, (c,))), ("ddt_bias", dt_bias, (f32, (c,)))):
+        if t is not None:
+            want[name] = what
+    _check_grads(want, out, workspace, named + [(dy, "dy"), (h0, "h0"), (dh_T, "dh_T")], dev)
+    shape, need = _ssm_plan(SSM_BWD, b, T, c, n, g, 0, int(bool(softplus)), *lds, _dt(ty), F32)
+    with _on(dev, stream) as st:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if out is None:
+            out = {name: torch.empty(sh, dtype=t, device=dev) for name, (t, sh) in want.items()}
+        grads = GdnSsmGrads(**{name: _addr(out[name]) for name in want})
+        _check(lib().gdn_ssm_bwd(shape, given, _addr(h0), _addr(dy), _addr(dh_T), grads, _addr(ws), ws.numel(), st),
+               "gdn_ssm_bwd")
+    return out
+
+
+def ssm_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, softplus=True, o_dtype=torch.float32, out=None,
+             stream=None):
+    """One token of every row (gdn_ssm_step), for decoding: x, dt, z [R,c]; B, C
+    [R,G,N]; state [n_slots,c,N] fp32, a pool advanced in place; slots as in
+    step.  Returns y [R,c] o_dtype."""
+    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 1)
+    dev, rows = x.device, x.shape[0]
+    n_slots = _leading(state, "state", 3)[0]
+    _check_tensors(dev, (state, "state", torch.float32, (n_slots, c, n)))
+    if slots is not None:
+        _check_tensors(dev, (slots, "slots", torch.int32, (rows,)))
+    if out is not None:
+        _check_tensors(dev, (out, "y", o_dtype, (rows, c)))
+        _check_apart(((out, "y"),), named + [(state, "state"), (slots, "slots")])
+    shape, _ = _ssm_plan(None, rows, 1, c, n, g, n_slots, int(bool(softplus)), *lds, _dt(x.dtype), _dt(o_dtype))
+    with _on(dev, stream) as st:
+        y = torch.empty((rows, c), dtype=o_dtype, device=dev) if out is None else out
+        _check(lib().gdn_ssm_step(shape, given, _addr(slots), _addr(state), _addr(y), st), "gdn_ssm_step")
+    return y
+
+
+# ---------------------------------------------------------------------------
+# verification of drafted tokens
+
+
+@functools.lru_cache(maxsize=256)
+def _verify_plan(*sizes):
+    shape = GdnVerifyShape(*sizes)
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_workspace_size_verify(shape, ctypes.byref(n)), "gdn_workspace_size_verify")
+    return shape, int(n.value)
+
+
+def tree_verify(tokens, parents, target, uniform, draft=None, workspace=None, stream=None):
+    """The verification of a tree of drafted tokens (gdn_tree_verify): walks
+    every row's tree from the root, accepting a node with the chance that makes
+    the accepted tokens, and the next one, distributed as the target's.
+
+    tokens, parents [B,n] int32 (parents as in tree_fwd, n <= 64); target
+    [B,n+1,V] fp32 probabilities: behind the root, then behind each node;
+    uniform [B,n+1] fp32 in [0, 1): one number per node, and the last for the
+    next token; draft [B,n,V] fp32: the probabilities that siblings were drawn
+    from, in the order of target, or None for tokens chosen without chance.
+    Returns int32 (last [B]: the last node accepted, -1 for none, as tree_commit
+    takes it; token [B]: the next token, -1 where the target has no mass;
+    path [B,n]: the nodes accepted, in order, then -1)."""
+    b, n = _leading(tokens, "tokens", 2)
+    dev, v = tokens.device, _leading(target, "target", 3)[2]
+    _check_tensors(dev, (tokens, "tokens", torch.int32, (b, n)), (parents, "parents", torch.int32, (b, n)),
+                   (target, "target", torch.float32, (b, n + 1, v)), (uniform, "uniform", torch.float32, (b, n + 1)))
+    if draft is not None:
+        _check_tensors(dev, (draft, "draft", torch.float32, (b, n, v)))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+        _check_apart(((workspace, "workspace"),), ((tokens, "tokens"), (parents, "parents"), (target, "target"),
+                                                   (uniform, "uniform"), (draft, "draft")))
+    shape, need = _verify_plan(b, n, v)
+    with _on(dev, stream) as st:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        whole = torch.empty((n + 2) * b, dtype=torch.int32, device=dev)   # one allocation for the three
+        last, token, path = whole[:b], whole[b:2 * b], whole[2 * b:].view(b, n)
+        _check(lib().gdn_tree_verify(shape, _addr(tokens), _addr(parents), _addr(target), _addr(draft), _addr(uniform),
+                                     _addr(last), _addr(token), _addr(path), _addr(ws), ws.numel(), st), "gdn_tree_verify")
+    return last, token, path

@@ -3,13 +3,15 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_api.hip"), os.path.join(CSRC, "gdn_states.hip"),
-           os.path.join(CSRC, "gdn_linear.hip")]
+           os.path.join(CSRC, "gdn_linear.hip"), os.path.join(CSRC, "gdn_conv.hip"),
+           os.path.join(CSRC, "gdn_ssm.hip"), os.path.join(CSRC, "gdn_verify.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -22,10 +24,22 @@ HIPCC_FLAGS = [
 def build(verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = LIB + ".tmp"
-    cmd = [hipcc] + HIPCC_FLAGS + SOURCES + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(prefix="gdn_build_") as work:   # the sources side by side, then one link
+        objects = [os.path.join(work, os.path.basename(src) + ".o") for src in SOURCES]
+        running = []
+        for src, obj in zip(SOURCES, objects):
+            cmd = [hipcc] + flags + ["-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append((cmd, subprocess.Popen(cmd)))
+        failed = [cmd for cmd, p in running if p.wait()]
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
+        cmd = [hipcc, "-shared"] + objects + ["-o", tmp]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,183 @@
+// gdn_conv.hip -- C ABI of the short causal convolution (declared in
+// include/gdn.h): argument checks and launches on the caller's stream.  No
+// allocation, no synchronisation.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "gdn.h"
+#include "gdn_conv.h"
+#include "gdn_host.h"
+
+using namespace gdn;
+
+namespace {
+
+constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of 256 threads: a launch holds fewer than 2^32
+constexpr int kFwdRun = 16, kBwdRun = 32;         // tokens per thread
+
+int elem(const gdn_conv_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
+
+gdn_status validate_conv(const gdn_conv_shape *s) {
+  if (!s) return GDN_ERR_NULL;
+  if (s->dtype != GDN_F32 && s->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (s->B < 1 || s->T < 0 || s->T > 1 << 30 || s->C < 1 || s->C > 1 << 24 || s->W < 2 || s->W > 4) return GDN_ERR_SHAPE;
+  if ((s->ld && s->ld < s->C) || (s->silu & ~1)) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+
+// every pointer at least an element of its type aligned
+gdn_status aligned(const gdn_conv_shape &s, std::initializer_list<const void *> data, std::initializer_list<const void *> f32) {
+  for (const void *p : data)
+    if (p && (uintptr_t)p % elem(s)) return GDN_ERR_ALIGN;
+  for (const void *p : f32)
+    if (p && (uintptr_t)p % 4) return GDN_ERR_ALIGN;
+  return GDN_OK;
+}
+// 16-byte pieces where the rows of everything are whole pieces, single elements else
+bool wide(const gdn_conv_shape &s, std::initializer_list<const void *> data) {
+  const int64_t e = elem(s);
+  bool ok = s.C * e % 16 == 0 && s.ld * e % 16 == 0;
+  for (const void *p : data) ok = ok && (uintptr_t)p % 16 == 0;
+  return ok;
+}
+
+ConvArgs conv_args(const gdn_conv_shape &s) {
+  ConvArgs a{};
+  a.B = s.B; a.T = s.T; a.C = s.C; a.n_slots = s.n_slots; a.silu = s.silu;
+  a.ld = s.ld ? s.ld : s.C;
+  return a;
+}
+// 64 threads side by side in channels, fewer where there are fewer
+void lay_out(ConvArgs &a, int vec, int rows, int run) {
+  const int groups = (a.C + vec - 1) / vec;
+  a.lane_bits = 0;
+  while (a.lane_bits < 6 && (1 << a.lane_bits) < groups) ++a.lane_bits;
+  a.lanes = 1 << a.lane_bits;
+  a.run = run;
+  const int64_t per = (int64_t)(256 >> a.lane_bits) * run;
+  a.runs = (int)((a.T + per - 1) / per);
+  (void)rows;
+}
+int tiles_of(const ConvArgs &a, int vec) { return (a.C / vec + a.lanes - 1) / a.lanes; }
+
+template <typename F>
+gdn_status with_width(int W, F &&f) {
+  return W == 2 ? f(std::integral_constant<int, 2>{}) : W == 3 ? f(std::integral_constant<int, 3>{}) : f(std::integral_constant<int, 4>{});
+}
+template <typename F>
+gdn_status with_pack(const gdn_conv_shape &s, bool wide, F &&f) {
+  if (s.dtype == GDN_BF16) return wide ? f(std::integral_constant<int, 8>{}, __bf16{}) : f(std::integral_constant<int, 1>{}, __bf16{});
+  return wide ? f(std::integral_constant<int, 4>{}, float{}) : f(std::integral_constant<int, 1>{}, float{});
+}
+
+gdn_status conv_fwd(const gdn_conv_shape *s, bool packed, const int32_t *cu, const void *x, const float *weight, const float *bias,
+                    const void *h0, void *y, void *h_T, void *hip_stream) {
+  GDN_TRY(validate_conv(s));
+  if ((s->T > 0 && (!x || !y)) || !weight || (packed && !cu)) return GDN_ERR_NULL;
+  GDN_TRY(aligned(*s, {x, h0, y, h_T}, {weight, bias, cu}));
+  if (s->T == 0 && !h_T) return GDN_OK;
+  ConvArgs a = conv_args(*s);
+  a.cu = packed ? cu : nullptr;
+  a.x = x; a.weight = weight; a.bias = bias; a.h0 = h0; a.y = y; a.h_T = h_T;
+  const int rows = packed ? 1 : s->B;
+  return with_pack(*s, wide(*s, {x, h0, y, h_T}), [&](auto vec, auto t) -> gdn_status {
+    constexpr int VEC = decltype(vec)::value;
+    using T = decltype(t);
+    lay_out(a, VEC, rows, kFwdRun);
+    const int per = 256 >> a.lane_bits;
+    const int64_t windows = h_T ? ((int64_t)s->B * (s->W - 1) + per - 1) / per : 0;
+    const int64_t blocks = ((int64_t)rows * a.runs + windows) * tiles_of(a, VEC);
+    if (blocks > kMaxBlocks) return GDN_ERR_SHAPE;
+    return with_width(s->W, [&](auto w) -> gdn_status {
+      hipLaunchKernelGGL((conv_fwd_kernel<decltype(w)::value, VEC, T>), dim3((unsigned)blocks), dim3(256), 0,
+                         reinterpret_cast<hipStream_t>(hip_stream), a);
+      return check_launch();
+    });
+  });
+}
+
+struct ConvPieces {
+  int64_t pieces;
+  size_t bytes;
+};
+ConvPieces pieces_of(const gdn_conv_shape &s, ConvArgs &a, int vec) {
+  lay_out(a, vec, s.B, kBwdRun);
+  a.runs = std::max(a.runs, 1);   // (an empty row still writes dh0)
+  const int64_t pieces = (int64_t)s.B * a.runs;
+  return {pieces, align_up((size_t)pieces * (s.W + 1) * s.C * 4)};
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_conv_fwd(const gdn_conv_shape *s, const void *x, const float *weight, const float *bias, const void *h0, void *y,
+                        void *h_T, void *hip_stream) {
+  return conv_fwd(s, false, nullptr, x, weight, bias, h0, y, h_T, hip_stream);
+}
+
+gdn_status gdn_conv_fwd_varlen(const gdn_conv_shape *s, const int32_t *cu_seqlens, const void *x, const float *weight,
+                               const float *bias, const void *h0, void *y, void *h_T, void *hip_stream) {
+  return conv_fwd(s, true, cu_seqlens, x, weight, bias, h0, y, h_T, hip_stream);
+}
+
+gdn_status gdn_conv_step(const gdn_conv_shape *s, const void *x, const float *weight, const float *bias, const int32_t *slots,
+                         void *state, void *y, void *hip_stream) {
+  GDN_TRY(validate_conv(s));
+  if (s->T != 1 || s->n_slots < 1 || (!slots && s->n_slots < s->B)) return GDN_ERR_SHAPE;
+  if (!x || !weight || !state || !y) return GDN_ERR_NULL;
+  GDN_TRY(aligned(*s, {x, state, y}, {weight, bias, slots}));
+  ConvArgs a = conv_args(*s);
+  a.x = x; a.weight = weight; a.bias = bias; a.slots = slots; a.state = state; a.y = y;
+  return with_pack(*s, wide(*s, {x, state, y}), [&](auto vec, auto t) -> gdn_status {
+    constexpr int VEC = decltype(vec)::value;
+    using T = decltype(t);
+    const int64_t blocks = (int64_t)s->B * ((s->C / VEC + 255) / 256);
+    if (blocks > kMaxBlocks) return GDN_ERR_SHAPE;
+    return with_width(s->W, [&](auto w) -> gdn_status {
+      hipLaunchKernelGGL((conv_step_kernel<decltype(w)::value, VEC, T>), dim3((unsigned)blocks), dim3(256), 0,
+                         reinterpret_cast<hipStream_t>(hip_stream), a);
+      return check_launch();
+    });
+  });
+}
+
+gdn_status gdn_workspace_size_conv_bwd(const gdn_conv_shape *s, size_t *bytes) {
+  if (!bytes) return GDN_ERR_NULL;
+  GDN_TRY(validate_conv(s));
+  // of the two layouts (16-byte pieces or single elements), the larger one
+  ConvArgs a = conv_args(*s);
+  const size_t one = pieces_of(*s, a, 1).bytes, many = pieces_of(*s, a, s->dtype == GDN_BF16 ? 8 : 4).bytes;
+  *bytes = std::max(one, many);
+  return GDN_OK;
+}
+
+gdn_status gdn_conv_bwd(const gdn_conv_shape *s, const void *x, const float *weight, const float *bias, const void *h0, const void *dy,
+                        const void *dh_T, void *dx, float *dweight, float *dbias, void *dh0, void *ws, size_t ws_bytes,
+                        void *hip_stream) {
+  GDN_TRY(validate_conv(s));
+  if ((s->T > 0 && (!x || !dy || !dx)) || !weight || !dweight || !ws) return GDN_ERR_NULL;
+  GDN_TRY(aligned(*s, {x, h0, dy, dh_T, dx, dh0}, {weight, bias, dweight, dbias, ws}));
+  ConvArgs a = conv_args(*s);
+  a.x = x; a.weight = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dh0 = dh0;
+  a.part = static_cast<float *>(ws);
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  return with_pack(*s, wide(*s, {x, h0, dy, dh_T, dx, dh0}), [&](auto vec, auto t) -> gdn_status {
+    constexpr int VEC = decltype(vec)::value;
+    using T = decltype(t);
+    const ConvPieces p = pieces_of(*s, a, VEC);
+    const int64_t blocks = p.pieces * tiles_of(a, VEC);
+    if (blocks > kMaxBlocks) return GDN_ERR_SHAPE;
+    if (ws_bytes < p.bytes) return GDN_ERR_WORKSPACE;
+    GDN_TRY(with_width(s->W, [&](auto w) -> gdn_status {
+      hipLaunchKernelGGL((conv_bwd_kernel<decltype(w)::value, VEC, T>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+      return check_launch();
+    }));
+    hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)((s->C + 63) / 64 * (s->W + 1))), dim3(1024), 0, st, a.part, (int)p.pieces, s->C,
+                       s->W, dweight, dbias);
+    return check_launch();
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,62 @@
+// gdn_verify.hip -- C ABI of the verification of drafted tokens (declared in
+// include/gdn.h): argument checks and launches on the caller's stream.  No
+// allocation, no synchronisation.
+#include <hip/hip_runtime.h>
+
+#include "gdn.h"
+#include "gdn_host.h"
+#include "gdn_verify.h"
+
+using namespace gdn;
+
+namespace {
+
+gdn_status validate_verify(const gdn_verify_shape *s) {
+  if (!s) return GDN_ERR_NULL;
+  if (s->B < 1 || s->n < 1 || s->n > kVerifyNodes || s->V < 1 || s->V > 1 << 24) return GDN_ERR_SHAPE;
+  // a launch holds fewer than 2^32 threads
+  if (s->B > 1 << 20 || (int64_t)s->B * ((s->V + VERIFY_PART - 1) / VERIFY_PART) > (1 << 23)) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+size_t plan_bytes(const gdn_verify_shape &s) { return align_up((size_t)s.B * sizeof(VerifyPlan)); }
+int parts_of(const gdn_verify_shape &s) { return (s.V + VERIFY_PART - 1) / VERIFY_PART; }
+size_t bytes_of(const gdn_verify_shape &s) { return plan_bytes(s) + align_up((size_t)s.B * parts_of(s) * 8); }
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_workspace_size_verify(const gdn_verify_shape *s, size_t *bytes) {
+  if (!bytes) return GDN_ERR_NULL;
+  GDN_TRY(validate_verify(s));
+  *bytes = bytes_of(*s);
+  return GDN_OK;
+}
+
+gdn_status gdn_tree_verify(const gdn_verify_shape *s, const int32_t *tokens, const int32_t *parents, const float *target,
+                           const float *draft, const float *uniform, int32_t *last, int32_t *token, int32_t *path, void *ws,
+                           size_t ws_bytes, void *hip_stream) {
+  GDN_TRY(validate_verify(s));
+  if (!tokens || !parents || !target || !uniform || !last || !token || !path || !ws) return GDN_ERR_NULL;
+  for (const void *p : {(const void *)tokens, (const void *)parents, (const void *)target, (const void *)draft, (const void *)uniform,
+                        (const void *)last, (const void *)token, (const void *)path})
+    if (p && (uintptr_t)p % 4) return GDN_ERR_ALIGN;
+  if (misaligned(ws)) return GDN_ERR_ALIGN;
+  if (ws_bytes < bytes_of(*s)) return GDN_ERR_WORKSPACE;
+  VerifyArgs a{};
+  a.B = s->B; a.n = s->n; a.V = s->V; a.parts = parts_of(*s);
+  a.tokens = tokens; a.parents = parents; a.target = target; a.draft = draft; a.uniform = uniform;
+  a.last = last; a.token = token; a.path = path;
+  a.plan = static_cast<VerifyPlan *>(ws);
+  a.part = reinterpret_cast<double *>(static_cast<char *>(ws) + plan_bytes(*s));
+  hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+  if (draft) hipLaunchKernelGGL(verify_walk_kernel<1024>, dim3((unsigned)s->B), dim3(1024), 0, st, a);
+  else hipLaunchKernelGGL(verify_walk_kernel<64>, dim3((unsigned)s->B), dim3(64), 0, st, a);
+  GDN_TRY(check_launch());
+  hipLaunchKernelGGL(verify_sum_kernel, dim3((unsigned)(s->B * a.parts)), dim3(256), 0, st, a);
+  GDN_TRY(check_launch());
+  hipLaunchKernelGGL(verify_draw_kernel, dim3((unsigned)s->B), dim3(256), 0, st, a);
+  return check_launch();
+}
+
+}  // extern "C"
