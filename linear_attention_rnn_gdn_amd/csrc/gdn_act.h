@@ -5,17 +5,16 @@
 
 namespace gdn {
 
-constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = 1.92596299112661746e-8f, kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f, kLn2Low = -1.9046542e-9f;
 
-// e^-|v| to a few units in the last place whatever |v|: the product with
-// log2(e) is carried with its rounding error (two fma), whose factor is 1 to
-// first order.
+// e^-|v| to a few units in the last place whatever |v|: e^w = 2^p e^{w - p ln 2}
+// with p = w log2(e) rounded, and the second factor, within 2^-17 of one, to
+// first order.  Below e^-128 zero, as fp32 has it.  (No number gives zero here;
+// the sums and products that follow carry it.)
 __device__ __forceinline__ float exp_neg_abs(float v) {
-  const float w = -fabsf(v), p = w * kLog2e;
-  const float low = fmaf(w, kLog2eLow, fmaf(w, kLog2e, -p));
+  const float w = fmaxf(-fabsf(v), -128.f), p = w * kLog2e;
   const float e = __builtin_amdgcn_exp2f(p);
-  const float f = fmaf(e, low * kLn2, e);
-  return p > -150.f ? f : e;   // (below: e is zero, and low no number at -inf)
+  return fmaf(e, fmaf(-p, kLn2Low, fmaf(-p, kLn2, w)), e);
 }
 
 struct Sigmoid {
@@ -25,7 +24,13 @@ __device__ __forceinline__ Sigmoid sigmoid_of(float v, float e) {   // e = e^-|v
   const float r = __builtin_amdgcn_rcpf(1.f + e), q = e * r;
   return v >= 0.f ? Sigmoid{r, q} : Sigmoid{q, r};
 }
-__device__ __forceinline__ float silu(float v) { return v * sigmoid_of(v, exp_neg_abs(v)).s; }
+// silu to fp32 accuracy; or (ROUGH), for a result that is rounded to bf16, to
+// |v| 2^-22 of itself, which that rounding's 2^-9 hides: half the instructions
+template <bool ROUGH = false>
+__device__ __forceinline__ float silu(float v) {
+  if constexpr (ROUGH) return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
+  else return v * sigmoid_of(v, exp_neg_abs(v)).s;
+}
 // silu and its derivative  s (1 + v (1 - s))
 __device__ __forceinline__ void silu_grad(float v, float &y, float &dy) {
   const Sigmoid g = sigmoid_of(v, exp_neg_abs(v));
@@ -33,20 +38,13 @@ __device__ __forceinline__ void silu_grad(float v, float &y, float &dy) {
   dy = fmaf(v * g.s, g.c, g.s);
 }
 
-// log(1 + e^v) = max(v, 0) + log1p(e^-|v|), and log1p(e) = 2 atanh(s) with
-// s = e / (2 + e) <= 1/3: seven terms of the odd series leave s^14 / 15 <
-// 2^-25 of it.  Small steps keep their relative accuracy, which the logarithm
-// of a rounded 1 + e would not.
+// log(1 + e^v) = max(v, 0) + log1p(e^-|v|).  With w = 1 + e rounded, log1p(e) =
+// log(w) + log1p((e - (w - 1)) / w): the rounding of w, which is all of e where
+// a step is small, is added back (e <= 1, so leaving out the division by w
+// changes that by less than 2^-25 of log(w)).
 __device__ __forceinline__ float softplus(float v, float e) {
-  const float s = e * __builtin_amdgcn_rcpf(2.f + e), p = s * s;
-  float q = 1.f / 13;
-  q = fmaf(q, p, 1.f / 11);
-  q = fmaf(q, p, 1.f / 9);
-  q = fmaf(q, p, 1.f / 7);
-  q = fmaf(q, p, 1.f / 5);
-  q = fmaf(q, p, 1.f / 3);
-  q = fmaf(q, p, 1.f);
-  return fmaf(2.f * s, q, fmaxf(v, 0.f));
+  const float w = 1.f + e, lost = e - (w - 1.f);
+  return fmaf(__builtin_amdgcn_logf(w), kLn2, lost) + __builtin_elementwise_maximum(v, 0.f);
 }
 
 // Sequences packed along one row of T tokens: sequence s holds tokens cu[s] ..

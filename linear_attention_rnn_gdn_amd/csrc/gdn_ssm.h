@@ -45,22 +45,32 @@ struct SsmArgs {
 template <typename T> using Uniform = const __attribute__((address_space(4))) T *;
 template <typename T> __device__ __forceinline__ Uniform<T> uniform(const T *p) { return (Uniform<T>)(uintptr_t)p; }
 
-// B or C of one token
-template <int N>
-__device__ __forceinline__ void load_row(const float *p, float (&x)[N]) {
-  Uniform<float> q = uniform(p);
+// B or C of one token, as it lies in memory: N scalar registers of fp32, half
+// as many of pairs of bf16, which are widened by scalar instructions (other
+// units than the vector ALU's).
+template <int N, typename TI> struct Row {
+  static constexpr int WORDS = N * sizeof(TI) / 4;
+  unsigned w[WORDS];
+  __device__ __forceinline__ void load(const TI *p) {
+    const Uniform<unsigned> q = uniform(reinterpret_cast<const unsigned *>(p));
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = q[i];
-}
-template <int N>
-__device__ __forceinline__ void load_row(const __bf16 *p, float (&x)[N]) {
-  Uniform<unsigned> q = uniform(reinterpret_cast<const unsigned *>(p));
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const unsigned w = q[i];
-    x[2 * i] = __builtin_bit_cast(float, w << 16);
-    x[2 * i + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
+    for (int i = 0; i < WORDS; ++i) w[i] = q[i];
   }
+  __device__ __forceinline__ float at(int n) const {
+    if constexpr (WORDS == N) return __builtin_bit_cast(float, w[n]);
+    const unsigned v = w[n / 2];
+    return n & 1 ? __builtin_bit_cast(float, v & 0xffff0000u) : __builtin_bit_cast(float, v << 16);
+  }
+  // Waits until the row is here.  Scalar loads return in any order, so a wait
+  // is for all of them: what is asked for next has to be asked for behind it.
+  __device__ __forceinline__ void wait() const { asm volatile("" ::"s"(w[0]), "s"(w[WORDS - 1])); }
+};
+template <int N, typename TI>
+__device__ __forceinline__ void load_row(const TI *p, float (&x)[N]) {
+  Row<N, TI> r;
+  r.load(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = r.at(i);
 }
 
 // An element at a lane's byte offset from a row that is the same for the whole
@@ -68,6 +78,17 @@ __device__ __forceinline__ void load_row(const __bf16 *p, float (&x)[N]) {
 template <typename T>
 __device__ __forceinline__ float get(const T *row, unsigned off) {
   return to_f32(*reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + off));
+}
+// (Hides an offset's value, once per group of loads: or the compiler adds it to
+// each tensor's address ahead of the loop and then 64-bit addresses per lane to
+// those, an instruction of the vector ALU per load.)
+__device__ __forceinline__ unsigned fresh_offset(unsigned off) {
+  asm volatile("" : "+v"(off));
+  return off;
+}
+template <typename T>
+__device__ __forceinline__ T raw(const T *row, unsigned off) {
+  return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + off);
 }
 template <typename T>
 __device__ __forceinline__ void put(T *row, unsigned off, float x) {
@@ -101,21 +122,30 @@ __device__ __forceinline__ void store_states(float *p, const float (&h)[N]) {
 
 __device__ __forceinline__ float step_size(const SsmArgs &a, float v) { return a.softplus ? softplus(v, exp_neg_abs(v)) : v; }
 
-constexpr int SSM_BATCH = 8;   // tokens asked for at once
+constexpr int SSM_BATCH = 4;   // tokens asked for at once, and worked on without a branch between them
 
 // One wave: 64 channels of one segment.  FOLD: only the segment's end state
-// and sum of d.
+// and sum of d.  The elements of the next SSM_BATCH tokens are on their way
+// while these are worked on, and so are B and C of the next token.
+// A batch in which the segment or a sequence ends is walked token by token.
+//
+// u B could come from the matrix cores (a lane's channel is a column of
+// v_mfma_f32_32x32x2's result, its states the rows), which takes 16
+// multiply-adds off the vector ALU; measured, the matrix instruction holds up
+// as many cycles of it, and the walk takes as long.
 template <int N, typename TI, typename TO, bool FOLD>
-__global__ __launch_bounds__(64) void ssm_walk_kernel(SsmArgs a) {
+__global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
   const int lane = threadIdx.x;
   const int tile = blockIdx.x % a.tiles;
   const int64_t unit = blockIdx.x / a.tiles;   // (row, segment)
   const Tile tl = tile_of(a, tile, lane);
   const int c = tl.c;
+  float h[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) h[n] = 0.f;
   if (!FOLD && unit >= (int64_t)a.rows * a.J) {   // empty sequences keep their state
     const int s = (int)(unit - (int64_t)a.rows * a.J);
     if (a.T && (!a.cu || offset_at(a.cu, s + 1, a.T) > offset_at(a.cu, s, a.T))) return;
-    float h[N] = {};
     const size_t at = ((size_t)s * a.C + c) * N;
     if (a.h0) load_states<N>(a.h0 + at, h);
     if (tl.on) store_states<N>(a.h_T + at, h);
@@ -125,89 +155,142 @@ __global__ __launch_bounds__(64) void ssm_walk_kernel(SsmArgs a) {
   if (FOLD && j + 1 == a.J) return;   // (nothing comes behind the last one)
   const int t0 = j * a.len, t1 = min(a.T, t0 + a.len);
   Sequence q{row, 0, a.T};
-  if (a.cu) {
-    q = sequence_at(a.cu, a.B, a.T, t0, 0);
+  auto next_sequence = [&](int t, int from) {
+    q = sequence_at(a.cu, a.B, a.T, t, from);
     q.seq = __builtin_amdgcn_readfirstlane(q.seq);
     q.begin = __builtin_amdgcn_readfirstlane(q.begin);
     q.end = __builtin_amdgcn_readfirstlane(q.end);
-  }
-  const int64_t r0 = (int64_t)row * a.T;
+  };
+  if (a.cu) next_sequence(t0, 0);
+  const int64_t r0 = (int64_t)row * a.T + t0;   // the segment's first token
+  const bool gated = a.z != nullptr;             // (without a gate x stands in for z, and is not used)
+  const int64_t ld_z = gated ? a.ld_z : a.ld_x;
   const TI *x = static_cast<const TI *>(a.x) + r0 * a.ld_x;
   const TI *dt = static_cast<const TI *>(a.dt) + r0 * a.ld_dt;
-  const bool gated = a.z != nullptr;
-  const TI *z = gated ? static_cast<const TI *>(a.z) + r0 * a.ld_z : nullptr;
+  const TI *z = static_cast<const TI *>(gated ? a.z : a.x) + r0 * ld_z;
   const TI *Bm = static_cast<const TI *>(a.Bm) + r0 * a.ld_b + tl.group * N;
   const TI *Cm = static_cast<const TI *>(a.Cm) + r0 * a.ld_c + tl.group * N;
   TO *y = static_cast<TO *>(a.y) + r0 * a.C;
   const unsigned ci = c * sizeof(TI), co = c * sizeof(TO);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
-  float A[N], h[N];   // A in units of log2(e)
+  float A[N];   // in units of log2(e)
   load_states<N>(a.A + (size_t)c * N, A);
 #pragma unroll
   for (int n = 0; n < N; ++n) A[n] *= kLog2e;
   const size_t su = ((size_t)unit * a.tiles + tile) * 64 + lane;   // among the segments' sums
   const size_t se = ((size_t)unit * a.tiles + tile) * N * 64 + lane;
   auto enter = [&]() {   // the state a sequence starts from
-    if (a.h0) load_states<N>(a.h0 + ((size_t)q.seq * a.C + c) * N, h);
-    else
+    if (a.h0) {
+      load_states<N>(a.h0 + ((size_t)q.seq * a.C + c) * N, h);
+#pragma unroll
+      for (int n = 0; n < N; ++n) asm volatile("" : "+v"(h[n]));   // (waits here, not at every use behind the join)
+    } else {
 #pragma unroll
       for (int n = 0; n < N; ++n) h[n] = 0.f;
+    }
   };
   bool fresh = q.begin == t0;
-  if (fresh) {
-    enter();
-  } else {
+  if (fresh) enter();
+  else if constexpr (!FOLD)
 #pragma unroll
-    for (int n = 0; n < N; ++n) h[n] = FOLD ? 0.f : a.in[se + n * 64];
-  }
+    for (int n = 0; n < N; ++n) h[n] = a.in[se + n * 64];
   float sum = 0.f;
-  int t = t0;
-  while (t < t1) {
-    const int stop = min(t1, q.end);
-    for (; t < stop; t += SSM_BATCH) {
-      float xs[SSM_BATCH], ds[SSM_BATCH], zs[SSM_BATCH];
+  struct Batch {
+    TI x[SSM_BATCH], dt[SSM_BATCH], z[SSM_BATCH];
+  };
+  // asks for the elements of the tokens from the pointers' on (past the segment's last: of that one again)
+  auto ask = [&](int left, Batch &p) {
+    const unsigned off = fresh_offset(ci);
 #pragma unroll
-      for (int i = 0; i < SSM_BATCH; ++i) {
-        const int64_t at = min(t + i, stop - 1);
-        xs[i] = get(x + at * a.ld_x, ci);
-        ds[i] = get(dt + at * a.ld_dt, ci);
-        if constexpr (!FOLD) zs[i] = gated ? get(z + at * a.ld_z, ci) : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < SSM_BATCH; ++i) {
-        if (t + i >= stop) break;
-        float b[N], cc[N];
-        load_row<N>(Bm + (int64_t)(t + i) * a.ld_b, b);
-        if constexpr (!FOLD) load_row<N>(Cm + (int64_t)(t + i) * a.ld_c, cc);
-        const float d = step_size(a, ds[i] + bias), u = d * xs[i];
-        float o[4] = {D * xs[i], 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          h[n] = fmaf(__builtin_amdgcn_exp2f(d * A[n]), h[n], u * b[n]);
-          if constexpr (!FOLD) o[n & 3] = fmaf(cc[n], h[n], o[n & 3]);
-        }
-        if constexpr (FOLD) {
-          sum += d;
-        } else {
-          float s = (o[0] + o[1]) + (o[2] + o[3]);
-          if (gated) s *= silu(zs[i]);
-          if (tl.on) put(y + (int64_t)(t + i) * a.C, co, s);
-        }
-      }
+    for (int i = 0; i < SSM_BATCH; ++i) {
+      const int64_t at = min(i, left - 1);
+      p.x[i] = raw(x + at * a.ld_x, off);
+      p.dt[i] = raw(dt + at * a.ld_dt, off);
+      if constexpr (!FOLD) p.z[i] = raw(z + at * ld_z, off);
     }
-    t = stop;
-    if (stop == q.end) {
+  };
+  // B and C of a token, and of the next, where scalar registers hold that
+  constexpr bool AHEAD = Row<N, TI>::WORDS <= 16;
+  Row<N, TI> B, C, Bn, Cn;
+  auto ask_rows = [&](Row<N, TI> &B, Row<N, TI> &C) {
+    B.load(Bm);
+    if constexpr (!FOLD) C.load(Cm);
+  };
+  if (AHEAD && t0 < t1) ask_rows(B, C);
+  Batch now, next;
+  if (t0 < t1) ask(t1 - t0, now);
+  for (int t = t0; t < t1; t += SSM_BATCH) {
+    const bool whole = t + SSM_BATCH <= t1 && (q.end <= t || q.end >= t + SSM_BATCH);
+    x += SSM_BATCH * a.ld_x;
+    dt += SSM_BATCH * a.ld_dt;
+    z += SSM_BATCH * ld_z;
+    if (t + SSM_BATCH < t1) ask(t1 - t - SSM_BATCH, next);
+    float xs[SSM_BATCH], d[SSM_BATCH];
+#pragma unroll
+    for (int i = 0; i < SSM_BATCH; ++i) {
+      xs[i] = to_f32(now.x[i]);
+      d[i] = step_size(a, to_f32(now.dt[i]) + bias);
+    }
+    auto token = [&](int i) {
+      if constexpr (AHEAD) {
+        B.wait();
+        if constexpr (!FOLD) C.wait();
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        ask_rows(B, C);
+      }
+      if (t + i + 1 < t1) {
+        Bm += a.ld_b;
+        Cm += a.ld_c;
+      }
+      if constexpr (AHEAD) {
+        ask_rows(Bn, Cn);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const float u = d[i] * xs[i];
+      float o[4] = {D * xs[i], 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        h[n] = fmaf(__builtin_amdgcn_exp2f(d[i] * A[n]), h[n], u * B.at(n));
+        if constexpr (!FOLD) o[n & 3] = fmaf(C.at(n), h[n], o[n & 3]);
+      }
+      if constexpr (FOLD) {
+        sum += d[i];
+      } else {
+        float s = (o[0] + o[1]) + (o[2] + o[3]);
+        s *= gated ? silu<std::is_same<TO, __bf16>::value>(to_f32(now.z[i])) : 1.f;
+        if (tl.on) put(y, fresh_offset(co), s);
+        y += a.C;
+      }
+      if constexpr (AHEAD) {
+        B = Bn;
+        if constexpr (!FOLD) C = Cn;
+      }
+    };
+    auto sequence_end = [&](int i) {
+      if (t + i + 1 != q.end) return;
       if constexpr (!FOLD)
         if (a.h_T && tl.on) store_states<N>(a.h_T + ((size_t)q.seq * a.C + c) * N, h);
-      if (stop < t1) {   // packed: the next sequence
-        q = sequence_at(a.cu, a.B, a.T, t, q.seq + 1);
-        q.seq = __builtin_amdgcn_readfirstlane(q.seq);
-        q.end = __builtin_amdgcn_readfirstlane(q.end);
+      if (q.end < t1) {   // packed: the next sequence
+        next_sequence(q.end, q.seq + 1);
         fresh = true;
         sum = 0.f;
         enter();
       }
+    };
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < SSM_BATCH; ++i) token(i);
+      sequence_end(SSM_BATCH - 1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SSM_BATCH; ++i) {
+        if (t + i >= t1) break;
+        token(i);
+        sequence_end(i);
+      }
     }
+    now = next;
   }
   if constexpr (FOLD) {
     a.sum[su] = sum;
@@ -217,23 +300,64 @@ __global__ __launch_bounds__(64) void ssm_walk_kernel(SsmArgs a) {
   }
 }
 
-// The states entering the segments: one thread per (row, channel, state),
-// from segment to segment.  Segment j's own state is complete where a sequence
-// begins in it.
+// The states entering the segments (or, REV, the cotangents entering them from
+// behind, from the last one on).  A workgroup takes one (row, 64 channels,
+// state): its four waves fold a quarter of the segments each, exchange what
+// they folded and go over them again from what enters their quarter.  Segment
+// j's own state is complete where a sequence begins in it.
+constexpr int SCAN_AHEAD = 16;   // segments asked for at once
 template <int N>
 __global__ __launch_bounds__(256) void ssm_scan_kernel(SsmArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), lanes = (int64_t)a.tiles * N;
-  if (i >= a.rows * lanes) return;
-  const int row = (int)(i / lanes), tile = (int)(i % lanes) / N, n = (int)(i % N);
-  const float A = a.A[(size_t)tile_of(a, tile, lane).c * N + n] * kLog2e;
-  float h = 0.f;
-  for (int j = 0; j + 1 < a.J; ++j) {
-    const size_t u = (size_t)row * a.J + j, v = u * a.tiles + tile;
-    const float e = a.end[(v * N + n) * 64 + lane], s = a.sum[v * 64 + lane];
-    h = a.fresh[u] ? e : fmaf(__builtin_amdgcn_exp2f(s * A), h, e);
-    a.in[((v + a.tiles) * N + n) * 64 + lane] = h;
+  __shared__ float folded[2][4][64];
+  __shared__ int begins[4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t all = (int64_t)a.rows * a.tiles * N;
+  const bool rev = blockIdx.x >= all;   // (the second half of the grid, where there is one)
+  const int64_t i = blockIdx.x - (rev ? all : 0);
+  const int n = (int)(i % N), tile = (int)(i / N % a.tiles), row = (int)(i / N / a.tiles);
+  const int c = tile_of(a, tile, lane).c;
+  const float A = a.A[(size_t)c * N + n] * kLog2e;
+  const float *end = rev ? a.rend : a.end;
+  float *in = rev ? a.rin : a.in;
+  const int steps = a.J - 1, per = (steps + 3) / 4, k0 = min(steps, wave * per), k1 = min(steps, k0 + per);
+  const int64_t first = rev ? a.J - 1 : 0, way = rev ? -1 : 1;   // step k: segment first + way k
+  float h = 0.f, sum = 0.f;   // this quarter's own state, and the sum of d over it
+  bool begun = false;         // a sequence begins in it
+  float e[SCAN_AHEAD], s[SCAN_AHEAD];
+  int fresh[SCAN_AHEAD];
+  auto ask = [&](int k) {
+#pragma unroll
+    for (int m = 0; m < SCAN_AHEAD; ++m) {
+      const int64_t u = row * (int64_t)a.J + first + way * min(k + m, steps - 1), v = u * a.tiles + tile;
+      e[m] = end[(v * N + n) * 64 + lane];
+      s[m] = a.sum[v * 64 + lane];
+      fresh[m] = !rev && a.fresh[u];
+    }
+  };
+  auto pass = [&](bool write) {
+    for (int k = k0; k < k1; k += SCAN_AHEAD) {
+      if (!write || k1 - k0 > SCAN_AHEAD) ask(k);   // (the second time a single batch is still here)
+#pragma unroll
+      for (int m = 0; m < SCAN_AHEAD; ++m) {
+        if (k + m >= k1) break;
+        h = fresh[m] ? e[m] : fmaf(__builtin_amdgcn_exp2f(s[m] * A), h, e[m]);
+        sum += s[m];
+        begun = begun || fresh[m];
+        if (write) in[(((row * (int64_t)a.J + first + way * (k + m + 1)) * a.tiles + tile) * N + n) * 64 + lane] = h;
+      }
+    }
+  };
+  pass(false);
+  folded[0][wave][lane] = h;
+  folded[1][wave][lane] = sum;
+  if (lane == 0) begins[wave] = begun;
+  __syncthreads();
+  h = rev && a.dh_T ? a.dh_T[((size_t)row * a.C + c) * N + n] : 0.f;
+  for (int w = 0; w < wave; ++w) {
+    const float f = folded[0][w][lane];
+    h = begins[w] ? f : fmaf(__builtin_amdgcn_exp2f(folded[1][w][lane] * A), h, f);
   }
+  pass(true);
 }
 
 // ----------------------------------------------------------------------------
@@ -293,23 +417,26 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
 // the product of the decays so far, the cotangent that leaves the segment at
 // its front is sum_t P_t C_t ds_t.
 template <int N, typename TI>
-__global__ __launch_bounds__(64) void ssm_bwd_fold_kernel(SsmArgs a) {
+__global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
+  using R = Row<N, TI>;
+  constexpr bool AHEAD = R::WORDS <= 16;
   const int lane = threadIdx.x, tile = blockIdx.x % a.tiles;
   const int64_t unit = blockIdx.x / a.tiles;
   const Tile tl = tile_of(a, tile, lane);
   const int c = tl.c, row = (int)(unit / a.J), j = (int)(unit % a.J);
-  const int t0 = j * a.len, t1 = min(a.T, t0 + a.len);
-  const int64_t r0 = (int64_t)row * a.T;
+  const int t0 = j * a.len, len = min(a.T - t0, a.len);
+  const int64_t r0 = (int64_t)row * a.T + t0;
+  const bool gated = a.z != nullptr;   // (without a gate x stands in for z, and is not used)
+  const int64_t ld_z = gated ? a.ld_z : a.ld_x;
   const TI *x = static_cast<const TI *>(a.x) + r0 * a.ld_x;
   const TI *dt = static_cast<const TI *>(a.dt) + r0 * a.ld_dt;
-  const bool gated = a.z != nullptr;
-  const TI *z = gated ? static_cast<const TI *>(a.z) + r0 * a.ld_z : nullptr;
+  const TI *z = static_cast<const TI *>(gated ? a.z : a.x) + r0 * ld_z;
   const TI *dy = static_cast<const TI *>(a.dy) + r0 * a.C;
-  const unsigned ci = c * sizeof(TI);
   const TI *Bm = static_cast<const TI *>(a.Bm) + r0 * a.ld_b + tl.group * N;
   const TI *Cm = static_cast<const TI *>(a.Cm) + r0 * a.ld_c + tl.group * N;
+  const unsigned ci = c * sizeof(TI);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-  float A[N], h[N], P[N], R[N];
+  float A[N], h[N], P[N], Q[N];
   load_states<N>(a.A + (size_t)c * N, A);
   if (j == 0 && a.h0) load_states<N>(a.h0 + ((size_t)row * a.C + c) * N, h);
   else
@@ -319,62 +446,78 @@ __global__ __launch_bounds__(64) void ssm_bwd_fold_kernel(SsmArgs a) {
   for (int n = 0; n < N; ++n) {
     A[n] *= kLog2e;
     P[n] = 1.f;
-    R[n] = 0.f;
+    Q[n] = 0.f;
   }
   float sum = 0.f;
-  for (int t = t0; t < t1; t += SSM_BATCH) {
-    float xs[SSM_BATCH], ds[SSM_BATCH], zs[SSM_BATCH], gs[SSM_BATCH];
+  struct Batch {
+    TI x[SSM_BATCH], dt[SSM_BATCH], z[SSM_BATCH], dy[SSM_BATCH];
+  };
+  auto ask = [&](int k, Batch &p) {
+    const unsigned off = fresh_offset(ci);
 #pragma unroll
     for (int i = 0; i < SSM_BATCH; ++i) {
-      const int64_t at = min(t + i, t1 - 1);
-      xs[i] = get(x + at * a.ld_x, ci);
-      ds[i] = get(dt + at * a.ld_dt, ci);
-      zs[i] = gated ? get(z + at * a.ld_z, ci) : 0.f;
-      gs[i] = get(dy + at * a.C, ci);
+      const int64_t at = min(k + i, len - 1);
+      p.x[i] = raw(x + at * a.ld_x, off);
+      p.dt[i] = raw(dt + at * a.ld_dt, off);
+      p.z[i] = raw(z + at * ld_z, off);
+      p.dy[i] = raw(dy + at * a.C, off);
+    }
+  };
+  R B, C, Bn, Cn;
+  Batch now, next;
+  ask(0, now);   // (a segment that is folded has a token)
+  if (AHEAD) {
+    B.load(Bm);
+    C.load(Cm);
+  }
+  for (int k = 0; k < len; k += SSM_BATCH) {
+    if (k + SSM_BATCH < len) ask(k + SSM_BATCH, next);
+    float d[SSM_BATCH], u[SSM_BATCH], g[SSM_BATCH];
+#pragma unroll
+    for (int i = 0; i < SSM_BATCH; ++i) {   // (a token past the last: no step, no cotangent)
+      const bool here = k + i < len;
+      d[i] = here ? step_size(a, to_f32(now.dt[i]) + bias) : 0.f;
+      u[i] = here ? d[i] * to_f32(now.x[i]) : 0.f;
+      g[i] = here ? to_f32(now.dy[i]) : 0.f;
+      g[i] *= gated ? silu<std::is_same<TI, __bf16>::value>(to_f32(now.z[i])) : 1.f;
+      sum += d[i];
     }
 #pragma unroll
     for (int i = 0; i < SSM_BATCH; ++i) {
-      if (t + i >= t1) break;
-      float b[N], cc[N];
-      load_row<N>(Bm + (int64_t)(t + i) * a.ld_b, b);
-      load_row<N>(Cm + (int64_t)(t + i) * a.ld_c, cc);
-      const float d = step_size(a, ds[i] + bias), u = d * xs[i];
-      const float g = gated ? gs[i] * silu(zs[i]) : gs[i];
-      sum += d;
+      const int64_t at = min(k + i + (AHEAD ? 1 : 0), len - 1);
+      if constexpr (AHEAD) {
+        B.wait();
+        C.wait();
+        __builtin_amdgcn_sched_barrier(0);
+        Bn.load(Bm + at * a.ld_b);
+        Cn.load(Cm + at * a.ld_c);
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        B.load(Bm + at * a.ld_b);
+        C.load(Cm + at * a.ld_c);
+      }
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float e = __builtin_amdgcn_exp2f(d * A[n]);
-        h[n] = fmaf(e, h[n], u * b[n]);
+        const float e = __builtin_amdgcn_exp2f(d[i] * A[n]);
+        h[n] = fmaf(e, h[n], u[i] * B.at(n));
         P[n] *= e;
-        R[n] = fmaf(P[n], g * cc[n], R[n]);
+        Q[n] = fmaf(P[n], g[i] * C.at(n), Q[n]);
+      }
+      if constexpr (AHEAD) {
+        B = Bn;
+        C = Cn;
       }
     }
+    now = next;
   }
   const size_t v = (size_t)unit * a.tiles + tile;
   a.sum[v * 64 + lane] = sum;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     a.end[(v * N + n) * 64 + lane] = h[n];
-    a.rend[(v * N + n) * 64 + lane] = R[n];
+    a.rend[(v * N + n) * 64 + lane] = Q[n];
   }
   if (tile == 0 && lane == 0) a.fresh[unit] = j == 0;
-}
-
-// the cotangents entering the segments from behind, from the last segment on
-template <int N>
-__global__ __launch_bounds__(256) void ssm_rscan_kernel(SsmArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), lanes = (int64_t)a.tiles * N;
-  if (i >= a.rows * lanes) return;
-  const int row = (int)(i / lanes), tile = (int)(i % lanes) / N, n = (int)(i % N);
-  const int c = tile_of(a, tile, lane).c;
-  const float A = a.A[(size_t)c * N + n] * kLog2e;
-  float g = a.dh_T ? a.dh_T[((size_t)row * a.C + c) * N + n] : 0.f;
-  for (int j = a.J - 1; j > 0; --j) {
-    const size_t v = ((size_t)row * a.J + j) * a.tiles + tile;
-    g = fmaf(__builtin_amdgcn_exp2f(a.sum[v * 64 + lane] * A), g, a.rend[(v * N + n) * 64 + lane]);
-    a.rin[((v - a.tiles) * N + n) * 64 + lane] = g;
-  }
 }
 
 // Sums of M values over the wave's 64 lanes: halves, quarters, .. of the
@@ -441,9 +584,12 @@ __device__ __forceinline__ int reduced_index(int lane) {
 template <int M> __device__ __forceinline__ bool reduced_writer(int lane) { return (lane & (64 / M - 1)) == 0; }
 
 // The way back over a segment takes pieces of S tokens, whose states a lane
-// holds in registers; the states at the pieces' fronts are kept in LDS (the
-// first one's can be read again).  Of 32 states a wave takes 16, and the two
-// waves of a channel exchange their sums over states once per piece.
+// holds in registers.  The states at every MARK-th token and the segment's
+// steps d stay in LDS from a first pass in token order; a piece that does not
+// begin at a mark walks to its front again.  (8 waves per compute unit have
+// 20 KB each; marks at every piece would take twice that and leave 5.)  Of 32
+// states a wave takes 16, and the two waves of a channel exchange their sums
+// over states once per piece.
 //
 // A lane's registers stay below 256, two waves per SIMD: with more, copies of
 // live values to accumulation registers are placed where paths join, and this
@@ -453,32 +599,36 @@ template <int M> __device__ __forceinline__ bool reduced_writer(int lane) { retu
 // other, and what differs between calls (a gate or none) branches on scalars,
 // never on lanes.
 template <int N> struct SsmBwd {
-  static constexpr int NS = N < 16 ? N : 16, WAVES = N / NS, S = NS == 8 ? 8 : 4, PIECES = 32 / S, LEN = S * PIECES;
+  static constexpr int NS = N < 16 ? N : 16, WAVES = N / NS, S = NS == 8 ? 8 : 4, MARK = 8, LEN = 32;
 };
 
 template <int N, typename TI>
 __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmArgs a) {
   using K = SsmBwd<N>;
-  constexpr int S = K::S, NS = K::NS;
-  __shared__ float marks[K::WAVES][K::PIECES - 1][NS][64];
-  __shared__ float sums[K::WAVES > 1 ? K::WAVES : 1][S][3][K::WAVES > 1 ? 64 : 1];
+  using R = Row<K::NS, TI>;
+  constexpr int S = K::S, NS = K::NS, LEN = K::LEN;
+  __shared__ float marks[K::WAVES][LEN / K::MARK - 1][NS][64];
+  __shared__ float steps[K::WAVES][LEN][64];
+  __shared__ float sums[K::WAVES][S][3][K::WAVES > 1 ? 64 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile = blockIdx.x % a.tiles;
   const int64_t unit = blockIdx.x / a.tiles;
   const Tile tl = tile_of(a, tile, lane);
   const int c = tl.c, row = (int)(unit / a.J), j = (int)(unit % a.J), n0 = wave * NS;
-  const int t0 = j * a.len, t1 = min(a.T, t0 + a.len);
-  const int64_t r0 = (int64_t)row * a.T;
-  const bool gated = a.z != nullptr;
+  const int t0 = j * a.len, len = min(a.T - t0, LEN);   // (a.len is LEN)
+  const int64_t r0 = (int64_t)row * a.T + t0;            // the segment's first token
+  const bool gated = a.z != nullptr;                      // (without a gate x stands in for z, and is not used)
+  const int64_t ld_z = gated ? a.ld_z : a.ld_x;
   const TI *x = static_cast<const TI *>(a.x) + r0 * a.ld_x;
   const TI *dt = static_cast<const TI *>(a.dt) + r0 * a.ld_dt;
-  const TI *z = gated ? static_cast<const TI *>(a.z) + r0 * a.ld_z : nullptr;
+  const TI *z = static_cast<const TI *>(gated ? a.z : a.x) + r0 * ld_z;
   const TI *dy = static_cast<const TI *>(a.dy) + r0 * a.C;
   const TI *Bm = static_cast<const TI *>(a.Bm) + r0 * a.ld_b + tl.group * N + n0;
   const TI *Cm = static_cast<const TI *>(a.Cm) + r0 * a.ld_c + tl.group * N + n0;
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
   const size_t v = (size_t)unit * a.tiles + tile, vn = (v * N + n0) * 64 + lane, sn = ((size_t)row * a.C + c) * N + n0;
-  float(*mark)[NS][64] = marks[wave];
   const unsigned ci = c * sizeof(TI), cr = reduced_index<NS>(lane) * 4;
+  float(*mark)[NS][64] = marks[wave];
+  float(*step)[64] = steps[wave];
   float A[NS], h[NS], dh[NS], dA[NS];
   load_states<NS>(a.A + (size_t)c * N + n0, A);
   auto front = [&]() {
@@ -505,92 +655,148 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
     dA[n] = 0.f;
   }
   float dD = 0.f, dbias = 0.f;
-  const int pieces = (t1 - t0 + S - 1) / S;
-  // forward over the segment: the state each piece starts from
-  front();
-  for (int k = 0; k + 1 < pieces; ++k) {
-    float xs[S], ds[S];
+  // a token of the way forward
+  auto advance = [&](float d, float xi, const R &B, float (&h)[NS]) {
+    const float u = d * xi;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int64_t at = t0 + k * S + i;
-      xs[i] = get(x + at * a.ld_x, ci);
-      ds[i] = get(dt + at * a.ld_dt, ci);
-    }
+    for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * A[n]), h[n], u * B.at(n));
+  };
+  // In token order: every step, and the states at the marks.  What comes next
+  // is asked for one batch (of x and dt) or token (of B) ahead.
+  {
+    constexpr int Q = SSM_BATCH;
+    TI xs[Q], ds[Q], xn[Q], dn[Q];
+    auto ask = [&](int k, TI(&xs)[Q], TI(&ds)[Q]) {
+      const unsigned off = fresh_offset(ci);
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      float b[NS];
-      load_row<NS>(Bm + (int64_t)(t0 + k * S + i) * a.ld_b, b);
-      const float d = step_size(a, ds[i] + bias), u = d * xs[i];
-#pragma unroll
-      for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * A[n]), h[n], u * b[n]);
-    }
-#pragma unroll
-    for (int n = 0; n < NS; ++n) mark[k][n][lane] = h[n];
-  }
-  for (int k = pieces - 1; k >= 0; --k) {
-    const int tk = t0 + k * S;
-    // per token: x, the step and its slope, the cotangent of s, and what s is multiplied with in dz
-    float xs[S], ds[S], slope[S], gs[S], ws[S], hs[S + 1][NS];
-    {
-      float zs[S];
-#pragma unroll
-      for (int i = 0; i < S; ++i) {   // (a token past the last: no step and no cotangent, so that it changes nothing)
-        const int64_t at = min(tk + i, t1 - 1);
-        const bool here = tk + i < t1 && tl.on;   // (nor does a lane past the last channel add to dB and dC)
-        xs[i] = get(x + at * a.ld_x, ci);
-        ds[i] = get(dt + at * a.ld_dt, ci);
-        gs[i] = get(dy + at * a.C, ci);
-        xs[i] = here ? xs[i] : 0.f;
-        gs[i] = here ? gs[i] : 0.f;
-        zs[i] = gated ? get(z + at * a.ld_z, ci) : 0.f;
+      for (int i = 0; i < Q; ++i) {
+        const int64_t at = max(min(k + i, len - 1), 0);
+        xs[i] = raw(x + at * a.ld_x, off);
+        ds[i] = raw(dt + at * a.ld_dt, off);
       }
+    };
+    R B, Bn;
+    if (len > 0) {
+      ask(0, xs, ds);
+      B.load(Bm);
+    }
+    front();
+    for (int k = 0; k < len; k += Q) {
+      if (k + Q < len) ask(k + Q, xn, dn);
+      float d[Q];
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        d[i] = step_size(a, to_f32(ds[i]) + bias);
+        step[k + i][lane] = d[i];   // (past the last token: its step again, not used)
+      }
+      if (k && k % K::MARK == 0)
+#pragma unroll
+        for (int n = 0; n < NS; ++n) mark[k / K::MARK - 1][n][lane] = h[n];
+      if (k / K::MARK < (len - 1) / K::MARK) {   // (nobody starts behind the last mark)
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          B.wait();
+          __builtin_amdgcn_sched_barrier(0);
+          Bn.load(Bm + (int64_t)min(k + i + 1, len - 1) * a.ld_b);
+          __builtin_amdgcn_sched_barrier(0);
+          advance(d[i], to_f32(xs[i]), B, h);
+          B = Bn;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        xs[i] = xn[i];
+        ds[i] = dn[i];
+      }
+    }
+  }
+  for (int k = (len - 1) / S * S; k >= 0 && len > 0; k -= S) {
+    // per token: x, the step, its slope, the cotangent of s, and what s is multiplied with in dz
+    float xs[S], ds[S], slope[S], gs[S], ws[S], hs[S + 1][NS];
+    R B, C, Bn, Cn;   // of a token, and of the one to be worked on next
+    auto row_of = [&](const TI *m, int64_t ld, int i) { return m + (int64_t)min(k + i, len - 1) * ld; };
+    {
+      TI xr[S], dr[S], gr[S], zr[S];
+      const unsigned off = fresh_offset(ci);
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const float e = exp_neg_abs(ds[i] + bias);
-        slope[i] = a.softplus ? sigmoid_of(ds[i] + bias, e).s : 1.f;
-        ds[i] = a.softplus ? softplus(ds[i] + bias, e) : ds[i] + bias;
-        ds[i] = tk + i < t1 ? ds[i] : 0.f;
+        const int64_t at = min(k + i, len - 1);
+        xr[i] = raw(x + at * a.ld_x, off);
+        dr[i] = raw(dt + at * a.ld_dt, off);
+        gr[i] = raw(dy + at * a.C, off);
+        zr[i] = raw(z + at * ld_z, off);
+      }
+      // the state at the piece's front
+      const int m = k / K::MARK;
+      if (m) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) hs[0][n] = mark[m - 1][n][lane];
+      } else {
+        front();
+#pragma unroll
+        for (int n = 0; n < NS; ++n) hs[0][n] = h[n];
+      }
+      if constexpr (S < K::MARK) {
+        if (k % K::MARK) {   // S tokens behind the mark
+          TI xm[S];
+#pragma unroll
+          for (int i = 0; i < S; ++i) xm[i] = raw(x + (int64_t)(k - S + i) * a.ld_x, off);
+#pragma unroll
+          for (int i = 0; i < S; ++i) {
+            R B;
+            B.load(Bm + (int64_t)(k - S + i) * a.ld_b);
+            advance(step[k - S + i][lane], to_f32(xm[i]), B, hs[0]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) {   // a token past the last, or a lane past the last channel: no step, no cotangent
+        const bool here = k + i < len;
+        const float e = exp_neg_abs(to_f32(dr[i]) + bias);
+        slope[i] = a.softplus ? sigmoid_of(to_f32(dr[i]) + bias, e).s : 1.f;
+        ds[i] = here ? step[min(k + i, LEN - 1)][lane] : 0.f;
+        xs[i] = here && tl.on ? to_f32(xr[i]) : 0.f;
+        const float g = here && tl.on ? to_f32(gr[i]) : 0.f;
         float sg, dsg;
-        silu_grad(zs[i], sg, dsg);
-        ws[i] = gs[i] * dsg;
-        gs[i] *= gated ? sg : 1.f;
+        silu_grad(to_f32(zr[i]), sg, dsg);
+        ws[i] = g * dsg;
+        gs[i] = gated ? g * sg : g;
       }
     }
-    if (k) {
-#pragma unroll
-      for (int n = 0; n < NS; ++n) hs[0][n] = mark[k - 1][n][lane];
-    } else {
-      front();
-#pragma unroll
-      for (int n = 0; n < NS; ++n) hs[0][n] = h[n];
-    }
+    B.load(row_of(Bm, a.ld_b, 0));
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      float b[NS];
-      load_row<NS>(Bm + (int64_t)min(tk + i, t1 - 1) * a.ld_b, b);
-      const float u = ds[i] * xs[i];
+      B.wait();
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 1 < S) Bn.load(row_of(Bm, a.ld_b, i + 1));
+      else C.load(row_of(Cm, a.ld_c, i));
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NS; ++n) hs[i + 1][n] = fmaf(__builtin_amdgcn_exp2f(ds[i] * A[n]), hs[i][n], u * b[n]);
+      for (int n = 0; n < NS; ++n) hs[i + 1][n] = hs[i][n];
+      advance(ds[i], xs[i], B, hs[i + 1]);
+      if (i + 1 < S) B = Bn;
       __builtin_amdgcn_sched_barrier(0);
     }
     float sum[S][3];   // over the states: s, du, dd
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-      float b[NS], cc[NS], r[NS];
-      int tt = min(tk + i, t1 - 1);
+      float r[NS];
       float d = ds[i];
-      // B and the decays are formed anew: kept from the way forward they would take S times as many registers
-      asm("" : "+s"(tt));
-      asm("" : "+v"(d));
-      const int64_t t = tt;
-      load_row<NS>(Bm + t * a.ld_b, b);
-      load_row<NS>(Cm + t * a.ld_c, cc);
+      asm("" : "+v"(d));   // (the decays are formed anew: kept from the way forward they would take S times NS registers)
+      B.wait();
+      C.wait();
+      __builtin_amdgcn_sched_barrier(0);
+      if (i) {
+        Bn.load(row_of(Bm, a.ld_b, i - 1));
+        Cn.load(row_of(Cm, a.ld_c, i - 1));
+      }
+      __builtin_amdgcn_sched_barrier(0);
       const float u = d * xs[i], g = gs[i];
-      float *to = a.part_bc + ((r0 + t) * a.tiles + tile) * 2 * N + n0;
+      float *to = a.part_bc + ((r0 + min(k + i, len - 1)) * a.tiles + tile) * 2 * N + n0;
       float s = 0.f, du = 0.f, dd = 0.f;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        s = fmaf(cc[n], hs[i + 1][n], s);
+        s = fmaf(C.at(n), hs[i + 1][n], s);
         r[n] = g * hs[i + 1][n];
       }
       reduce_lanes<NS>(r, lane);
@@ -598,16 +804,16 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        dh[n] = fmaf(cc[n], g, dh[n]);
+        dh[n] = fmaf(C.at(n), g, dh[n]);
         r[n] = u * dh[n];
-        du = fmaf(b[n], dh[n], du);
+        du = fmaf(B.at(n), dh[n], du);
         dh[n] *= __builtin_amdgcn_exp2f(d * A[n]);
         const float q = hs[i][n] * dh[n];
         dd = fmaf(A[n], q, dd);
         dA[n] = fmaf(d, q, dA[n]);
       }
       reduce_lanes<NS>(r, lane);
-      if (tk + i < t1 && reduced_writer<NS>(lane)) {
+      if (k + i < len && reduced_writer<NS>(lane)) {
         put(to, cr, r[0]);
         put(to + N, cr, rc);
       }
@@ -615,6 +821,10 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
       sum[i][0] = s;
       sum[i][1] = du;
       sum[i][2] = dd;
+      if (i) {
+        B = Bn;
+        C = Cn;
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (K::WAVES > 1) {
@@ -631,13 +841,13 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
     }
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      if (tk + i >= t1) break;
+      if (k + i >= len) break;
       const float g = gs[i], d = ds[i], s = fmaf(D, xs[i], sum[i][0]), du = sum[i][1];
       const float dv = fmaf(xs[i], du, sum[i][2] * kLn2) * slope[i];   // (A is in units of log2(e))
       dbias += dv;
       dD = fmaf(g, xs[i], dD);
       if (tl.on && (K::WAVES == 1 || (i & 1) == wave)) {
-        const int64_t at = (r0 + tk + i) * a.C;
+        const int64_t at = (r0 + k + i) * a.C;
         put(static_cast<TI *>(a.dx) + at, ci, fmaf(d, du, D * g));
         put(static_cast<TI *>(a.ddt) + at, ci, dv);
         if (gated) put(static_cast<TI *>(a.dz) + at, ci, ws[i] * s);
@@ -656,29 +866,48 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
   if (j == 0 && a.dh0) store_states<NS>(a.dh0 + sn, dh);
 }
 
-// dB and dC: the sums over a group's waves, one thread per element
+// dB and dC: the sums over a group's waves.  A wave takes one token and group,
+// 16 bytes of the 2 N values per lane, as many of the group's waves side by side
+// as that leaves room for.
 template <int N, typename TI>
 __global__ __launch_bounds__(256) void ssm_bc_sum_kernel(SsmArgs a, TI *dB, TI *dC, int64_t tokens) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= tokens * a.G * 2 * N) return;
-  const int n = (int)(i % (2 * N)), g = (int)(i / (2 * N) % a.G);
-  const int64_t t = i / (2 * N) / a.G;
+  constexpr int L = 2 * N / 4, R = 64 / L;   // lanes per row of values, rows at once
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane % L * 4;
+  const int64_t i = (int64_t)blockIdx.x * 4 + wave, t = i / a.G;
+  const int g = (int)(i % a.G);
+  if (t >= tokens) return;
   const float *p = a.part_bc + (t * a.tiles + g * a.per) * 2 * N + n;
-  float s = 0.f;
-  for (int k = 0; k < a.per; ++k) s += p[(size_t)k * 2 * N];
-  const int64_t at = (t * a.G + g) * N + n % N;
-  (n < N ? dB : dC)[at] = from_f32<TI>(s);
+  float4 s{0.f, 0.f, 0.f, 0.f};
+  for (int k = lane / L; k < a.per; k += R) {
+    const float4 v = *reinterpret_cast<const float4 *>(p + (size_t)k * 2 * N);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+#pragma unroll
+  for (int m = L; m < 64; m <<= 1) {
+    s.x += __shfl_xor(s.x, m); s.y += __shfl_xor(s.y, m); s.z += __shfl_xor(s.z, m); s.w += __shfl_xor(s.w, m);
+  }
+  if (lane >= L) return;
+  TI *to = (n < N ? dB : dC) + (t * a.G + g) * N + n % N;
+  if constexpr (std::is_same<TI, float>::value) *reinterpret_cast<float4 *>(to) = s;
+  else *reinterpret_cast<uint2 *>(to) = uint2{pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
 }
 
-// dA, dD and ddt_bias: the sums over the segments
+// dA, dD and ddt_bias: the sums over the segments, 64 channels of one of them
+// per workgroup, 16 segments side by side.
 template <int N>
-__global__ __launch_bounds__(256) void ssm_a_sum_kernel(SsmArgs a, float *dA, float *dD, float *dbias) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)(N + 2) * a.C) return;
-  const int n = (int)(i / a.C), c = (int)(i % a.C);
+__global__ __launch_bounds__(1024) void ssm_a_sum_kernel(SsmArgs a, float *dA, float *dD, float *dbias) {
+  __shared__ double red[16][64];
+  const int lane = threadIdx.x & 63, r = threadIdx.x >> 6, tiles = (a.C + 63) / 64;
+  const int n = blockIdx.x / tiles, c = blockIdx.x % tiles * 64 + lane;
   const int64_t units = (int64_t)a.rows * a.J;
   double s = 0.;
-  for (int64_t u = 0; u < units; ++u) s += (double)a.part_a[(size_t)u * (N + 2) * a.C + i];
+  if (c < a.C)
+    for (int64_t u = r; u < units; u += 16) s += (double)a.part_a[((size_t)u * (N + 2) + n) * a.C + c];
+  red[r][lane] = s;
+  __syncthreads();
+  if (r || c >= a.C) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += red[i][lane];
   if (n < N) dA[(size_t)c * N + n] = (float)s;
   else if (n == N) {
     if (dD) dD[c] = (float)s;

@@ -14,7 +14,7 @@ using namespace gdn;
 namespace {
 
 constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 threads
-constexpr int kWaves = 2048, kShortest = 32;
+constexpr int kWaves = 4096, kShortest = 32;
 
 int elem(const gdn_ssm_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 int64_t ld(int32_t given, int64_t dense) { return given ? given : dense; }
@@ -104,7 +104,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
 }
 gdn_status check_sizes(const gdn_ssm_shape &s, const SsmArgs &a, const Layout &l) {
   if (((int64_t)a.rows * l.J + s.B) * a.tiles > kMaxWaves) return GDN_ERR_SHAPE;
-  if ((int64_t)a.rows * a.tiles * s.N > kMaxWaves) return GDN_ERR_SHAPE;
+  if ((int64_t)a.rows * a.tiles * s.N > kMaxWaves / 8) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 void place(SsmArgs &a, const Layout &l, void *ws) {
@@ -115,7 +115,7 @@ void place(SsmArgs &a, const Layout &l, void *ws) {
   a.rend = reinterpret_cast<float *>(p + l.rend); a.rin = reinterpret_cast<float *>(p + l.rin);
   a.part_bc = reinterpret_cast<float *>(p + l.part_bc); a.part_a = reinterpret_cast<float *>(p + l.part_a);
 }
-unsigned scan_blocks(const SsmArgs &a) { return (unsigned)(((int64_t)a.rows * a.tiles * a.N + 3) / 4); }
+unsigned scan_blocks(const SsmArgs &a) { return (unsigned)((int64_t)a.rows * a.tiles * a.N); }
 
 gdn_status ssm_fwd(const gdn_ssm_shape *s, bool packed, const int32_t *cu, const gdn_ssm_inputs *in, const float *h0, void *y, float *h_T,
                    void *ws, size_t ws_bytes, void *hip_stream) {
@@ -210,7 +210,7 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *s, const gdn_ssm_inputs *in, const f
   SsmArgs a = ssm_args(*s, false);
   const Layout l = layout_ssm(*s, a, true);
   GDN_TRY(check_sizes(*s, a, l));
-  const int64_t tokens = (int64_t)s->B * s->T, bc = (tokens * s->G * 2 * s->N + 255) / 256;
+  const int64_t tokens = (int64_t)s->B * s->T, bc = (tokens * s->G + 3) / 4;
   if (bc > kMaxWaves / 4) return GDN_ERR_SHAPE;
   GDN_TRY(aligned(*s, {in->x, in->dt, in->z, dy, out->dx, out->ddt, out->dz}, {in->B, in->C, in->A, h0, dh_T, out->dB, out->dC, out->dA, out->dh0, ws}));
   for (const void *p : {(const void *)in->D, (const void *)in->dt_bias, (const void *)out->dD, (const void *)out->ddt_bias})
@@ -228,9 +228,7 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *s, const gdn_ssm_inputs *in, const f
       if (l.J > 1) {
         hipLaunchKernelGGL((ssm_bwd_fold_kernel<N, TI>), dim3(walks), dim3(64), 0, st, a);
         GDN_TRY(check_launch());
-        hipLaunchKernelGGL(ssm_scan_kernel<N>, dim3(scan_blocks(a)), dim3(256), 0, st, a);
-        GDN_TRY(check_launch());
-        hipLaunchKernelGGL(ssm_rscan_kernel<N>, dim3(scan_blocks(a)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(ssm_scan_kernel<N>, dim3(2 * scan_blocks(a)), dim3(256), 0, st, a);
         GDN_TRY(check_launch());
       }
       hipLaunchKernelGGL((ssm_bwd_kernel<N, TI>), dim3(walks), dim3(64 * SsmBwd<N>::WAVES), 0, st, a);
@@ -240,7 +238,7 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *s, const gdn_ssm_inputs *in, const f
                            static_cast<TI *>(out->dC), tokens);
         GDN_TRY(check_launch());
       }
-      hipLaunchKernelGGL(ssm_a_sum_kernel<N>, dim3((unsigned)(((int64_t)(N + 2) * s->C + 255) / 256)), dim3(256), 0, st, a, out->dA, out->dD,
+      hipLaunchKernelGGL(ssm_a_sum_kernel<N>, dim3((unsigned)((N + 2) * ((s->C + 63) / 64))), dim3(1024), 0, st, a, out->dA, out->dD,
                          out->ddt_bias);
       return check_launch();
     };
