@@ -7,35 +7,31 @@ namespace gdn {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f, kLn2Low = -1.9046542e-9f;
 
-// e^-|v| to a few units in the last place whatever |v|: e^w = 2^p e^{w - p ln 2}
-// with p = w log2(e) rounded, and the second factor, within 2^-17 of one, to
-// first order.  Below e^-128 zero, as fp32 has it.  (No number gives zero here;
-// the sums and products that follow carry it.)
-__device__ __forceinline__ float exp_neg_abs(float v) {
-  const float w = fmaxf(-fabsf(v), -128.f), p = w * kLog2e;
-  const float e = __builtin_amdgcn_exp2f(p);
-  return fmaf(e, fmaf(-p, kLn2Low, fmaf(-p, kLn2, w)), e);
+// e^w for |w| <= 128 (beyond fp32's range on both sides) to a few units in the
+// last place: 2^p e^{w - p ln 2} with p = w log2(e) rounded, and the second
+// factor, within 2^-17 of one, to first order.
+__device__ __forceinline__ float exp_to_ulps(float w) {
+  const float p = w * kLog2e;
+  return __builtin_amdgcn_exp2f(p) * (1.f + fmaf(-p, kLn2Low, fmaf(-p, kLn2, w)));
 }
-
-struct Sigmoid {
-  float s, c;   // sigmoid(v) and 1 - sigmoid(v), each to relative accuracy
-};
-__device__ __forceinline__ Sigmoid sigmoid_of(float v, float e) {   // e = e^-|v|
-  const float r = __builtin_amdgcn_rcpf(1.f + e), q = e * r;
-  return v >= 0.f ? Sigmoid{r, q} : Sigmoid{q, r};
+// (No number gives zero here, or one of the ends; the sums and products that
+// follow carry it.)
+__device__ __forceinline__ float exp_neg_abs(float v) { return exp_to_ulps(fmaxf(-fabsf(v), -128.f)); }
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.f + exp_to_ulps(__builtin_amdgcn_fmed3f(-v, -128.f, 128.f)));
 }
 // silu to fp32 accuracy; or (ROUGH), for a result that is rounded to bf16, to
 // |v| 2^-22 of itself, which that rounding's 2^-9 hides: half the instructions
 template <bool ROUGH = false>
 __device__ __forceinline__ float silu(float v) {
   if constexpr (ROUGH) return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
-  else return v * sigmoid_of(v, exp_neg_abs(v)).s;
+  else return v * sigmoid(v);
 }
 // silu and its derivative  s (1 + v (1 - s))
 __device__ __forceinline__ void silu_grad(float v, float &y, float &dy) {
-  const Sigmoid g = sigmoid_of(v, exp_neg_abs(v));
-  y = v * g.s;
-  dy = fmaf(v * g.s, g.c, g.s);
+  const float g = sigmoid(v);
+  y = v * g;
+  dy = fmaf(y, 1.f - g, g);
 }
 
 // log(1 + e^v) = max(v, 0) + log1p(e^-|v|).  With w = 1 + e rounded, log1p(e) =

@@ -752,8 +752,7 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
 #pragma unroll
       for (int i = 0; i < S; ++i) {   // a token past the last, or a lane past the last channel: no step, no cotangent
         const bool here = k + i < len;
-        const float e = exp_neg_abs(to_f32(dr[i]) + bias);
-        slope[i] = a.softplus ? sigmoid_of(to_f32(dr[i]) + bias, e).s : 1.f;
+        slope[i] = a.softplus ? sigmoid(to_f32(dr[i]) + bias) : 1.f;
         ds[i] = here ? step[min(k + i, LEN - 1)][lane] : 0.f;
         xs[i] = here && tl.on ? to_f32(xr[i]) : 0.f;
         const float g = here && tl.on ? to_f32(gr[i]) : 0.f;
