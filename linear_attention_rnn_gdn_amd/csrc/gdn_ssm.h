@@ -614,7 +614,7 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
   const int64_t unit = blockIdx.x / a.tiles;
   const Tile tl = tile_of(a, tile, lane);
   const int c = tl.c, row = (int)(unit / a.J), j = (int)(unit % a.J), n0 = wave * NS;
-  const int t0 = j * a.len, len = min(a.T - t0, LEN);   // (a.len is LEN)
+  const int t0 = j * a.len, len = min(a.T - t0, a.len);   // (LEN at most, whole marks)
   const int64_t r0 = (int64_t)row * a.T + t0;            // the segment's first token
   const bool gated = a.z != nullptr;                      // (without a gate x stands in for z, and is not used)
   const int64_t ld_z = gated ? a.ld_z : a.ld_x;

@@ -14,7 +14,7 @@ using namespace gdn;
 namespace {
 
 constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 threads
-constexpr int kWaves = 4096, kShortest = 32;
+constexpr int kWaves = 4096, kShortest = 16, kFew = 1536, kFewest = 128;
 
 int elem(const gdn_ssm_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 int64_t ld(int32_t given, int64_t dense) { return given ? given : dense; }
@@ -70,7 +70,8 @@ struct Layout {
 Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   Layout l{};
   if (grads) {
-    l.len = s.N == 8 ? SsmBwd<8>::LEN : s.N == 16 ? SsmBwd<16>::LEN : SsmBwd<32>::LEN;
+    const int64_t pieces = (int64_t)a.rows * a.tiles * ((s.T + 31) / 32);
+    l.len = pieces < kFewest ? 8 : pieces < kFew ? 16 : 32;
     l.J = std::max(1, (s.T + l.len - 1) / l.len);
   } else {
     const int64_t walks = (int64_t)a.rows * a.tiles, want = std::max<int64_t>(1, kWaves / walks);
