@@ -842,32 +842,33 @@ def _columns(t, name, dtype, shape, dev, tail):
     """Checks a tensor that may be columns of a wider one: the last ``tail``
     dimensions dense, the tokens before them evenly spaced.  Returns the
     elements from a token to the next (0: dense)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not (type(t) is torch.Tensor and t.get_device() == dev.index and t.dtype is dtype and t.shape == shape):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.is_contiguous():
         return 0
     strides, width = t.stride(), 1
-    for i in range(len(shape) - 1, len(shape) - 1 - tail, -1):
-        if shape[i] > 1 and strides[i] != width:
+    for i in range(1, tail + 1):
+        if strides[-i] != width and shape[-i] > 1:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
-        width *= shape[i]
-    ld = None
-    for i in range(len(shape) - 1 - tail, -1, -1):
-        if shape[i] == 1:
+        width *= shape[-i]
+    tokens, ld = strides[:-tail], None
+    for n, stride in zip(reversed(shape[:-tail]), reversed(tokens)):
+        if n == 1:
             continue
         if ld is None:
-            ld = after = strides[i]
-        elif strides[i] != after:
+            ld = after = stride
+        elif stride != after:
             raise ValueError(f"{name}: tokens must be evenly spaced")
-        after *= shape[i]
+        after *= n
     if ld is None:
         return 0
     if not width <= ld < 1 << 31:
@@ -994,7 +995,8 @@ def conv_bwd(x, weight, dy, bias=None, h0=None, dh_T=None, activation="silu", wo
         want["dbias"] = (torch.float32, (C,))
     shape, need = _conv_plan(True, B, T, C, W, ld, 0, silu, _dt(dt))
     inputs = ((x, "x"), (weight, "weight"), (bias, "bias"), (h0, "h0"), (dy, "dy"), (dh_T, "dh_T"))
-    _check_grads(want, out, workspace, inputs, dev)
+    if not (out is None and workspace is None):
+        _check_grads(want, out, workspace, inputs, dev)
     with _on(dev, stream) as st:
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
         if out is None:
@@ -1051,29 +1053,36 @@ def _ssm_plan(kind, *sizes):
     return shape, int(n.value)
 
 
-def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, lead):
-    """Checks the inputs of a scan or a step; returns its sizes (channels,
-    states, groups) and token strides, the C struct and the inputs' names."""
+def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, lead, others=()):
+    """Checks the inputs of a scan or a step, and ``others`` as _check_tensors
+    takes them; returns its sizes (channels, states, groups) and token strides,
+    and the C struct."""
     xs = _leading(x, "x", lead + 1)
-    _dt(x.dtype)
     dev, ty, c = x.device, x.dtype, xs[-1]
+    _dt(ty)
     n = _leading(A, "A", 2)[1]
     g = _leading(B, "B", lead + 2)[-2]
-    lds = [_columns(x, "x", ty, xs, dev, 1), _columns(dt, "dt", ty, xs, dev, 1),
-           0 if z is None else _columns(z, "z", ty, xs, dev, 1)]
-    lds += [_columns(t, name, ty, xs[:-1] + (g, n), dev, 2) for t, name in ((B, "B"), (C, "C"))]
-    _check_tensors(dev, (A, "A", torch.float32, (c, n)))
-    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _check_tensors(dev, (t, name, torch.float32, (c,)))
-    given = GdnSsmInputs(_addr(x), _addr(dt), _addr(z), _addr(B), _addr(C), _addr(A), _addr(D), _addr(dt_bias))
-    named = [(x, "x"), (dt, "dt"), (z, "z"), (B, "B"), (C, "C"), (A, "A"), (D, "D"), (dt_bias, "dt_bias")]
-    return (c, n, g), lds, given, named
+    rows = (*xs[:-1], g, n)
+    lds = (_columns(x, "x", ty, xs, dev, 1), _columns(dt, "dt", ty, xs, dev, 1),
+           0 if z is None else _columns(z, "z", ty, xs, dev, 1),
+           _columns(B, "B", ty, rows, dev, 2), _columns(C, "C", ty, rows, dev, 2))
+    items = [(A, "A", torch.float32, (c, n)), *others]
+    if D is not None:
+        items.append((D, "D", torch.float32, (c,)))
+    if dt_bias is not None:
+        items.append((dt_bias, "dt_bias", torch.float32, (c,)))
+    _check_tensors(dev, *items)
+    return (c, n, g), lds, GdnSsmInputs(x.data_ptr(), dt.data_ptr(), _addr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _addr(D),
+                                        _addr(dt_bias))
+
+
+def _ssm_names(x, dt, A, B, C, D, z, dt_bias):
+    return [(x, "x"), (dt, "dt"), (z, "z"), (B, "B"), (C, "C"), (A, "A"), (D, "D"), (dt_bias, "dt_bias")]
 
 
 def _ssm_fwd(rows, cu, x, dt, A, B, C, D, z, dt_bias, h0, softplus, o_dtype, output_final_state, workspace, out,
              final_state, stream):
-    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2)
+    (c, n, g), lds, given = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2)
     dev, (b, T, _) = x.device, x.shape
     seqs = b if rows is None else rows
     state = (seqs, c, n)
@@ -1083,7 +1092,8 @@ def _ssm_fwd(rows, cu, x, dt, A, B, C, D, z, dt_bias, h0, softplus, o_dtype, out
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, None, dev)
     if not (out is None and final_state is None and workspace is None):
-        _check_apart(((out, "y"), (final_state, "h_T"), (workspace, "workspace")), named + [(h0, "h0"), (cu, "cu_seqlens")])
+        _check_apart(((out, "y"), (final_state, "h_T"), (workspace, "workspace")),
+                     _ssm_names(x, dt, A, B, C, D, z, dt_bias) + [(h0, "h0"), (cu, "cu_seqlens")])
     shape, need = _ssm_plan(SSM_FWD if rows is None else SSM_VARLEN, seqs, T, c, n, g, 0, int(bool(softplus)), *lds,
                             _dt(x.dtype), _dt(o_dtype))
     with _on(dev, stream) as st:
@@ -1130,18 +1140,20 @@ def ssm_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None, dh_T=None
     dy [B,T,c] in x's dtype; h0, dh_T [B,c,N] fp32 or None.  Returns a dict
     (``out``: such a dict to write into): dx, ddt, dB, dC and, with z, dz in x's
     dtype; dA, dh0 and, where given, dD and ddt_bias fp32."""
-    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2)
-    dev, ty, (b, T, _) = x.device, x.dtype, x.shape
-    f32, row, state = torch.float32, (b, T, c), (b, c, n)
-    _check_tensors(dev, (dy, "dy", ty, row))
-    for t, name in ((h0, "h0"), (dh_T, "dh_T")):
-        if t is not None:
-            _check_tensors(dev, (t, name, f32, state))
+    b, T, c = _leading(x, "x", 3)
+    dev, ty, f32, row = x.device, x.dtype, torch.float32, (b, T, c)
+    others = [(dy, "dy", ty, row)]
+    if h0 is not None or dh_T is not None:
+        state = (b, c, _leading(A, "A", 2)[1])
+        others += [(t, name, f32, state) for t, name in ((h0, "h0"), (dh_T, "dh_T")) if t is not None]
+    (c, n, g), lds, given = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 2, others)
+    state = (b, c, n)
     want = dict(dx=(ty, row), ddt=(ty, row), dB=(ty, (b, T, g, n)), dC=(ty, (b, T, g, n)), dA=(f32, (c, n)), dh0=(f32, state))
     for name, t, what in (("dz", z, (ty, row)), ("dD", D, (f32, (c,))), ("ddt_bias", dt_bias, (f32, (c,)))):
         if t is not None:
             want[name] = what
-    _check_grads(want, out, workspace, named + [(dy, "dy"), (h0, "h0"), (dh_T, "dh_T")], dev)
+    if not (out is None and workspace is None):
+        _check_grads(want, out, workspace, _ssm_names(x, dt, A, B, C, D, z, dt_bias) + [(dy, "dy"), (h0, "h0"), (dh_T, "dh_T")], dev)
     shape, need = _ssm_plan(SSM_BWD, b, T, c, n, g, 0, int(bool(softplus)), *lds, _dt(ty), F32)
     with _on(dev, stream) as st:
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
@@ -1158,15 +1170,16 @@ def ssm_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, so
     """One token of every row (gdn_ssm_step), for decoding: x, dt, z [R,c]; B, C
     [R,G,N]; state [n_slots,c,N] fp32, a pool advanced in place; slots as in
     step.  Returns y [R,c] o_dtype."""
-    (c, n, g), lds, given, named = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 1)
-    dev, rows = x.device, x.shape[0]
-    n_slots = _leading(state, "state", 3)[0]
-    _check_tensors(dev, (state, "state", torch.float32, (n_slots, c, n)))
+    rows, c = _leading(x, "x", 2)
+    dev, n_slots = x.device, _leading(state, "state", 3)[0]
+    others = [(state, "state", torch.float32, (n_slots, c, _leading(A, "A", 2)[1]))]
     if slots is not None:
-        _check_tensors(dev, (slots, "slots", torch.int32, (rows,)))
+        others.append((slots, "slots", torch.int32, (rows,)))
     if out is not None:
-        _check_tensors(dev, (out, "y", o_dtype, (rows, c)))
-        _check_apart(((out, "y"),), named + [(state, "state"), (slots, "slots")])
+        others.append((out, "y", o_dtype, (rows, c)))
+    (c, n, g), lds, given = _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, 1, others)
+    if out is not None:
+        _check_apart(((out, "y"),), _ssm_names(x, dt, A, B, C, D, z, dt_bias) + [(state, "state"), (slots, "slots")])
     shape, _ = _ssm_plan(None, rows, 1, c, n, g, n_slots, int(bool(softplus)), *lds, _dt(x.dtype), _dt(o_dtype))
     with _on(dev, stream) as st:
         y = torch.empty((rows, c), dtype=o_dtype, device=dev) if out is None else out

@@ -65,6 +65,7 @@ constexpr int CONV_BATCH = 8, CONV_BWD_BATCH = 4;   // rows asked for at once
 template <int W, int VEC, typename T>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
   using P = typename Pack<T, VEC>::type;
+  constexpr bool ROUGH = std::is_same<T, __bf16>::value;
   const int tid = threadIdx.x, tiles = (a.C / VEC + a.lanes - 1) / a.lanes;
   const int tile = blockIdx.x % tiles;
   const int64_t piece = blockIdx.x / tiles;
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
         float s = bias[v];
 #pragma unroll
         for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-        o[v] = a.silu ? silu(s) : s;
+        o[v] = a.silu ? silu<ROUGH>(s) : s;
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
       }
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
   }
   if (a.silu)
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = silu(o[v]);
+    for (int v = 0; v < VEC; ++v) o[v] = silu<std::is_same<T, __bf16>::value>(o[v]);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) *reinterpret_cast<P *>(st + (size_t)k * a.C) = in[k + 1];
   *y = narrow<VEC, T>(o);

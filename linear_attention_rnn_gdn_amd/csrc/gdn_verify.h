@@ -31,7 +31,8 @@ constexpr int kVerifyNodes = 64;      // nodes per row: one per lane of a wave
 constexpr int VERIFY_PART = 4096;     // tokens of the vocabulary per workgroup and partial sum
 
 struct VerifyPlan {
-  double taken;                 // t above
+  double taken;                 // t above, of the last refusal
+  double before;                // t without it, if its residual's mass is not known yet; -1 else
   unsigned long long refused;   // without draft probabilities: the nodes whose tokens are taken out
   int at, pad;                  // the node reached, -1: the root
 };
@@ -65,73 +66,90 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
-__device__ __forceinline__ double shfl_f64(double x, int lane) { return __shfl(x, lane); }
-
-// The path of one row: one workgroup, every wave the same sweep.
-template <int THREADS>
-__global__ __launch_bounds__(THREADS) void verify_walk_kernel(VerifyArgs a) {
-  constexpr int WAVES = THREADS / 64;
-  __shared__ double red[2][WAVES];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.n;
+// The path of one row, every wave of the workgroup the same sweep.  A refusal
+// with no child behind it leaves its residual's mass to the sums that follow.
+template <int THREADS, bool DRAFT>
+__device__ __forceinline__ VerifyPlan verify_walk(const VerifyArgs &a, int b, int tid, double (&red)[2][THREADS / 64], int &mine) {
+  const int lane = tid & 63, wave = tid >> 6, n = a.n;
   const int parent = lane < n ? a.parents[(size_t)b * n + lane] : -2;
   const int x = lane < n ? a.tokens[(size_t)b * n + lane] : -1;
   const bool child = parent >= -1 && parent < lane && x >= 0 && x < a.V;
   double px = 0., qx = 0., u = 0.;
   if (child) {
     px = positive((double)a.target[((size_t)b * (n + 1) + parent + 1) * a.V + x]);
-    if (a.draft) qx = positive((double)a.draft[((size_t)b * n + parent + 1) * a.V + x]);
+    if constexpr (DRAFT) qx = positive((double)a.draft[((size_t)b * n + parent + 1) * a.V + x]);
     u = (double)a.uniform[(size_t)b * (n + 1) + lane];
   }
-  unsigned long long todo = __ballot(child), refused = 0;
-  int at = -1, len = 0, turn = 0, mine = -1;   // mine: this lane's entry of the path
-  double mass = 1., taken = 0.;
-  while (true) {
-    const unsigned long long next = __ballot((todo >> lane & 1) && parent == at);
-    if (!next) break;
+  VerifyPlan plan{0., -1., 0, -1, 0};
+  unsigned long long todo = __ballot(child);
+  int len = 0, turn = 0;
+  double mass = 1.;
+  mine = -1;   // this lane's entry of the path
+  unsigned long long next = __ballot(child && parent == -1);
+  while (next) {
     const int r = __ffsll((long long)next) - 1;
     todo &= ~(1ull << r);
-    const double p = shfl_f64(px, r), q = shfl_f64(qx, r), ur = shfl_f64(u, r);
-    const int xr = __shfl(x, r);
+    const double p = __shfl(px, r), q = __shfl(qx, r), ur = __shfl(u, r);
     bool ok;
-    if (a.draft) {
-      ok = ur * mass * q < positive(fma(-taken, q, p));
+    if constexpr (DRAFT) {
+      ok = ur * mass * q < positive(fma(-plan.taken, q, p));
     } else {
-      const bool again = __ballot((refused >> lane & 1) && x == xr) != 0;   // a sibling with this token was refused
+      const int xr = __shfl(x, r);
+      const bool again = __ballot((plan.refused >> lane & 1) && x == xr) != 0;   // a sibling with this token was refused
       const double left = again ? 0. : p;
       ok = ur * mass < left;
-      if (!ok) mass -= left;
+      if (!ok) {
+        mass -= left;
+        plan.refused |= 1ull << r;
+      }
     }
     if (ok) {
-      at = r;
+      plan = VerifyPlan{0., -1., 0, r, 0};
       if (lane == len) mine = r;
       ++len;
       mass = 1.;
-      taken = 0.;
-      refused = 0;
-    } else if (!a.draft) {
-      refused |= 1ull << r;
-    } else {
+    }
+    next = __ballot((todo >> lane & 1) && parent == plan.at);
+    if constexpr (DRAFT) {
+      if (ok) continue;
+      const double t = plan.taken + mass;
+      if (!next) {
+        plan.before = plan.taken;
+        plan.taken = t;
+        break;
+      }
       // the sum decides whether the residual is taken, and the next child's test
-      const double t = taken + mass;
-      const double w = wave_sum(residual_share<THREADS>(a.target + ((size_t)b * (n + 1) + at + 1) * a.V,
-                                                        a.draft + ((size_t)b * n + at + 1) * a.V, t, 0, a.V, tid));
+      const double w = wave_sum(residual_share<THREADS>(a.target + ((size_t)b * (n + 1) + plan.at + 1) * a.V,
+                                                        a.draft + ((size_t)b * n + plan.at + 1) * a.V, t, 0, a.V, tid));
       if (lane == 0) red[turn & 1][wave] = w;
       __syncthreads();
       double s = 0.;
-      for (int i = 0; i < WAVES; ++i) s += red[turn & 1][i];
+#pragma unroll
+      for (int i = 0; i < THREADS / 64; ++i) s += red[turn & 1][i];
       ++turn;
       if (s > 0.) {
-        taken = t;
+        plan.taken = t;
         mass = s;
       }
     }
   }
-  if (wave) return;
-  if (lane < n) a.path[(size_t)b * n + lane] = mine;
+  return plan;
+}
+__device__ __forceinline__ void note_walk(const VerifyArgs &a, int b, int lane, const VerifyPlan &plan, int mine) {
+  if (lane < a.n) a.path[(size_t)b * a.n + lane] = mine;
   if (lane == 0) {
-    a.last[b] = at;
-    a.plan[b] = VerifyPlan{taken, refused, at, 0};
+    a.last[b] = plan.at;
+    a.plan[b] = plan;
   }
+}
+
+// With draft probabilities, the walk in a launch of its own: its passes over
+// the vocabulary take a whole workgroup per row.
+__global__ __launch_bounds__(1024) void verify_walk_kernel(VerifyArgs a) {
+  __shared__ double red[2][16];
+  int mine;
+  const VerifyPlan plan = verify_walk<1024, true>(a, blockIdx.x, threadIdx.x, red, mine);
+  if (threadIdx.x < 64) note_walk(a, blockIdx.x, threadIdx.x, plan, mine);
 }
 
 // A part's weights: max(p - t q, 0), or p without the refused tokens.
@@ -141,79 +159,136 @@ struct Residual {
   const int *tokens;
   unsigned long long refused;   // those in the part
 };
-__device__ __forceinline__ Residual residual_of(const VerifyArgs &a, int b, int lo, int hi, int lane) {
-  const VerifyPlan w = a.plan[b];
+__device__ __forceinline__ Residual residual_of(const VerifyArgs &a, const VerifyPlan &w, double taken, int b, int lo, int hi, int lane) {
   Residual r;
   r.p = a.target + ((size_t)b * (a.n + 1) + w.at + 1) * a.V;
-  r.q = a.draft && w.taken > 0. ? a.draft + ((size_t)b * a.n + w.at + 1) * a.V : nullptr;
-  r.t = w.taken;
+  r.q = a.draft && taken > 0. ? a.draft + ((size_t)b * a.n + w.at + 1) * a.V : nullptr;
+  r.t = taken;
   r.tokens = a.tokens + (size_t)b * a.n;
   const int x = lane < a.n && (w.refused >> lane & 1) ? r.tokens[lane] : -1;
   r.refused = __ballot(x >= lo && x < hi);
   return r;
 }
-__device__ __forceinline__ double weight(const Residual &r, int v) {
-  double x = (double)r.p[v];
-  if (r.q) x = fma(-r.t, (double)r.q[v], x);
-  for (unsigned long long m = r.refused; m; m &= m - 1)
-    if (r.tokens[__ffsll((long long)m) - 1] == v) x = 0.;
-  return positive(x);
+// COUNT weights, tokens v, v + step, .. below hi (none behind it), all asked for at once
+template <int COUNT>
+__device__ __forceinline__ void weights(const Residual &r, int v, int step, int hi, double (&w)[COUNT]) {
+  float p[COUNT], q[COUNT];
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) {
+    const int at = min(v + i * step, hi - 1);
+    p[i] = r.p[at];
+    q[i] = r.q ? r.q[at] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) w[i] = v + i * step < hi ? positive(fma(-r.t, (double)q[i], (double)p[i])) : 0.;
+  for (unsigned long long m = r.refused; m; m &= m - 1) {   // (uniform, and mostly none)
+    const int x = r.tokens[__ffsll((long long)m) - 1];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) w[i] = v + i * step == x ? 0. : w[i];
+  }
+}
+// the sum over a part, by a wave
+__device__ __forceinline__ double part_sum(const Residual &r, int lo, int hi, int lane) {
+  constexpr int COUNT = 16;
+  double s = 0.;
+  for (int v = lo; v < hi; v += 64 * COUNT) {
+    double w[COUNT];
+    weights<COUNT>(r, v + lane, 64, hi, w);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) s += w[i];
+  }
+  return wave_sum(s);
 }
 
+// The sums of the parts, one workgroup each, a quarter per wave.  Without
+// draft probabilities every workgroup walks the tree first (a few reads of
+// single probabilities), which saves a launch.
+template <bool DRAFT>
 __global__ __launch_bounds__(256) void verify_sum_kernel(VerifyArgs a) {
   __shared__ double red[4];
-  const int b = blockIdx.x / a.parts, k = blockIdx.x % a.parts, tid = threadIdx.x, lane = tid & 63;
-  const int lo = k * VERIFY_PART, hi = min(a.V, lo + VERIFY_PART);
-  const Residual r = residual_of(a, b, lo, hi, lane);
-  double s = 0.;
-  for (int v = lo + tid; v < hi; v += 256) s += weight(r, v);
-  s = wave_sum(s);
-  if (lane == 0) red[tid >> 6] = s;
+  const int b = blockIdx.x / a.parts, k = blockIdx.x % a.parts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  VerifyPlan plan;
+  if constexpr (DRAFT) {
+    plan = a.plan[b];
+  } else {
+    double none[2][4];
+    int mine;
+    plan = verify_walk<256, false>(a, b, tid, none, mine);
+    if (k == 0 && wave == 0) note_walk(a, b, lane, plan, mine);
+  }
+  constexpr int QUARTER = VERIFY_PART / 4;
+  const int lo = min(a.V, k * VERIFY_PART + wave * QUARTER), hi = min(a.V, lo + QUARTER);
+  const Residual r = residual_of(a, plan, plan.taken, b, lo, hi, lane);
+  const double s = part_sum(r, lo, hi, lane);
+  if (lane == 0) red[wave] = s;
   __syncthreads();
   if (tid == 0) a.part[(size_t)b * a.parts + k] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// The token: the part in which the running sum passes u times the whole, then
-// the token within it.  Rounding may leave the part's own sums short of the
-// mark: its last token with a weight then.
+__device__ __forceinline__ double wave_scan(double x, int lane) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// The token: the part in which the running sum passes u times the whole, in it
+// the 16 tokens of a thread, among them the token.  Where rounding leaves sums
+// on one level short of the mark that the level above had passed, it is the
+// last one with a weight.
 __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a) {
   constexpr int PER = VERIFY_PART / 256;
-  __shared__ double red[4], scan[256];
-  __shared__ int found;
+  __shared__ double total[4], from;
+  __shared__ int found, hits[4], some[4];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const double *part = a.part + (size_t)b * a.parts;
-  // thread 0 .. 255: consecutive parts each
+  const VerifyPlan plan = a.plan[b];
+  double *part = a.part + (size_t)b * a.parts;
+  const double u = (double)a.uniform[(size_t)b * (a.n + 1) + a.n];
   const int per = (a.parts + 255) / 256, k0 = min(a.parts, tid * per), k1 = min(a.parts, k0 + per);
-  double s = 0.;
-  for (int k = k0; k < k1; ++k) s += part[k];
-  scan[tid] = s;
-  __syncthreads();
-  double before = 0., total = 0.;
-  for (int i = 0; i < 256; ++i) {
-    if (i == tid) before = total;
-    total += scan[i];
-  }
-  const double mark = (double)a.uniform[(size_t)b * (a.n + 1) + a.n] * total;
+  double taken = plan.taken, before, whole;
   if (tid == 0) found = -1;
-  __syncthreads();
+  for (bool again = false;; again = true) {
+    double s = 0.;
+    for (int k = k0; k < k1; ++k) s += part[k];
+    const double upto = wave_scan(s, lane);
+    if (lane == 63) total[wave] = upto;
+    __syncthreads();
+    before = upto - s;
+    whole = 0.;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += total[w];
+      whole += total[w];
+    }
+    if (whole > 0. || again || plan.before < 0.) break;   // uniform
+    // a residual without mass is not taken: the sums without the last refusal
+    taken = plan.before;
+    for (int k = wave; k < a.parts; k += 4) {
+      const int lo = k * VERIFY_PART, hi = min(a.V, lo + VERIFY_PART);
+      const double p = part_sum(residual_of(a, plan, taken, b, lo, hi, lane), lo, hi, lane);
+      if (lane == 0) part[k] = p;
+    }
+    __syncthreads();
+  }
+  const double mark = u * whole;
   int mine = -1;
   double start = 0., run = before;
   for (int k = k0; k < k1; ++k) {
-    if (mine < 0 && run + part[k] > mark && part[k] > 0.) {
+    if (mine < 0 && part[k] > 0. && run + part[k] > mark) {
       mine = k;
       start = run;
     }
     run += part[k];
   }
-  // the first thread whose parts pass the mark; if rounding leaves none, the last one with mass
-  const bool pass = mine >= 0;
+  // the first thread with such a part: of a wave, then of the waves
+  const unsigned long long pass = __ballot(mine >= 0);
   __shared__ int first[4];
-  __shared__ double from;
-  const unsigned long long bal = __ballot(pass);
-  if (lane == 0) first[wave] = bal ? wave * 64 + __ffsll((long long)bal) - 1 : 1 << 30;
+  if (lane == 0) first[wave] = pass ? wave * 64 + __ffsll((long long)pass) - 1 : 256;
   __syncthreads();
   const int who = min(min(first[0], first[1]), min(first[2], first[3]));
-  if (who == 1 << 30) {   // uniform: no mass (or no number)
+  if (who == 256) {   // uniform: no mass (or no number)
     if (tid == 0) a.token[b] = -1;
     return;
   }
@@ -223,31 +298,24 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a) {
   }
   __syncthreads();
   const int lo = found * VERIFY_PART, hi = min(a.V, lo + VERIFY_PART);
-  const Residual r = residual_of(a, b, lo, hi, lane);
+  const Residual r = residual_of(a, plan, taken, b, lo, hi, lane);
   double w[PER], sum = 0.;
+  weights<PER>(r, lo + tid * PER, 1, hi, w);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int v = lo + tid * PER + i;
-    w[i] = v < hi ? weight(r, v) : 0.;
-    sum += w[i];
-  }
-  double upto = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(upto, d);
-    if (lane >= d) upto += o;
-  }
-  if (lane == 63) red[wave] = upto;
+  for (int i = 0; i < PER; ++i) sum += w[i];
+  const double upto = wave_scan(sum, lane);
+  if (lane == 63) total[wave] = upto;
   __syncthreads();
-  double run2 = from + (upto - sum);
-  for (int i = 0; i < wave; ++i) run2 += red[i];
+  run = from + (upto - sum);
+  for (int i = 0; i < wave; ++i) run += total[i];
+  // this thread's first token with a weight at which the sum passes, and its last with a weight
   int hit = 1 << 30, any = -1;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    run2 += w[i];
+    run += w[i];
     if (w[i] > 0.) {
       any = lo + tid * PER + i;
-      if (run2 > mark) hit = min(hit, any);
+      if (run > mark) hit = min(hit, any);
     }
   }
 #pragma unroll
@@ -255,17 +323,14 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a) {
     hit = min(hit, __shfl_xor(hit, m));
     any = max(any, __shfl_xor(any, m));
   }
-  __shared__ int hits[4], anys[4];
   if (lane == 0) {
     hits[wave] = hit;
-    anys[wave] = any;
+    some[wave] = any;
   }
   __syncthreads();
-  if (tid == 0) {
-    hit = min(min(hits[0], hits[1]), min(hits[2], hits[3]));
-    any = max(max(anys[0], anys[1]), max(anys[2], anys[3]));
-    a.token[b] = hit < 1 << 30 ? hit : any;
-  }
+  if (tid) return;
+  hit = min(min(hits[0], hits[1]), min(hits[2], hits[3]));
+  a.token[b] = hit < 1 << 30 ? hit : max(max(some[0], some[1]), max(some[2], some[3]));
 }
 
 }  // namespace gdn

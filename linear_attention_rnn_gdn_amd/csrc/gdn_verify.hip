@@ -50,10 +50,14 @@ gdn_status gdn_tree_verify(const gdn_verify_shape *s, const int32_t *tokens, con
   a.plan = static_cast<VerifyPlan *>(ws);
   a.part = reinterpret_cast<double *>(static_cast<char *>(ws) + plan_bytes(*s));
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
-  if (draft) hipLaunchKernelGGL(verify_walk_kernel<1024>, dim3((unsigned)s->B), dim3(1024), 0, st, a);
-  else hipLaunchKernelGGL(verify_walk_kernel<64>, dim3((unsigned)s->B), dim3(64), 0, st, a);
-  GDN_TRY(check_launch());
-  hipLaunchKernelGGL(verify_sum_kernel, dim3((unsigned)(s->B * a.parts)), dim3(256), 0, st, a);
+  const dim3 parts((unsigned)(s->B * a.parts));
+  if (draft) {
+    hipLaunchKernelGGL(verify_walk_kernel, dim3((unsigned)s->B), dim3(1024), 0, st, a);
+    GDN_TRY(check_launch());
+    hipLaunchKernelGGL(verify_sum_kernel<true>, parts, dim3(256), 0, st, a);
+  } else {
+    hipLaunchKernelGGL(verify_sum_kernel<false>, parts, dim3(256), 0, st, a);
+  }
   GDN_TRY(check_launch());
   hipLaunchKernelGGL(verify_draw_kernel, dim3((unsigned)s->B), dim3(256), 0, st, a);
   return check_launch();
