@@ -20,16 +20,16 @@ __device__ __forceinline__ float exp_neg_abs(float v) { return exp_to_ulps(fmaxf
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.f + exp_to_ulps(__builtin_amdgcn_fmed3f(-v, -128.f, 128.f)));
 }
-// silu to fp32 accuracy; or (ROUGH), for a result that is rounded to bf16, to
-// |v| 2^-22 of itself, which that rounding's 2^-9 hides: half the instructions
-template <bool ROUGH = false>
-__device__ __forceinline__ float silu(float v) {
-  if constexpr (ROUGH) return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
-  else return v * sigmoid(v);
+// sigmoid of v (1 + a rounding): what the rounding of v log2(e) does to it is
+// what another rounding of v would do, so it is as good as v where v is a
+// rounded sum (or where the result is rounded to bf16), at half the instructions.
+__device__ __forceinline__ float sigmoid_rough(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
 }
+template <bool ROUGH> __device__ __forceinline__ float silu(float v) { return v * (ROUGH ? sigmoid_rough(v) : sigmoid(v)); }
 // silu and its derivative  s (1 + v (1 - s))
-__device__ __forceinline__ void silu_grad(float v, float &y, float &dy) {
-  const float g = sigmoid(v);
+template <bool ROUGH> __device__ __forceinline__ void silu_grad(float v, float &y, float &dy) {
+  const float g = ROUGH ? sigmoid_rough(v) : sigmoid(v);
   y = v * g;
   dy = fmaf(y, 1.f - g, g);
 }
@@ -53,18 +53,36 @@ __device__ __forceinline__ int offset_at(const int *cu, int s, int T) {
   const int v = cu[s];
   return v < 0 ? 0 : v > T ? T : v;
 }
-// The sequence of token t, which lies in [0, T); `from`: one at or before it.
-// Tokens behind the last offset count as the last sequence's.
-__device__ __forceinline__ Sequence sequence_at(const int *cu, int n, int T, int t, int from) {
+// The sequence of token t, which lies in [0, T).  Tokens behind the last offset
+// count as the last sequence's.  OFFSETS: anything that gives offset s in [0, n].
+template <typename Offsets>
+__device__ __forceinline__ Sequence sequence_of(const Offsets &cu, int n, int T, int t, int lo) {
+  const int b = cu(lo), e = cu(lo + 1);
+  return Sequence{lo, b < t ? b : t, e > t ? e : lo + 1 < n ? t + 1 : T};
+}
+// each thread for itself, by halving; `from`: one at or before it
+template <typename Offsets>
+__device__ __forceinline__ Sequence sequence_at(const Offsets &cu, int n, int T, int t, int from) {
   int lo = from < n ? from : n - 1, hi = n;   // the last one that begins at t or before
-  if (lo + 1 < n && offset_at(cu, lo + 1, T) > t) hi = lo + 1;
+  if (lo + 1 < n && cu(lo + 1) > t) hi = lo + 1;
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
-    if (offset_at(cu, mid, T) <= t) lo = mid;
+    if (cu(mid) <= t) lo = mid;
     else hi = mid;
   }
-  const int b = offset_at(cu, lo, T), e = offset_at(cu, lo + 1, T);
-  return Sequence{lo, b < t ? b : t, e > t ? e : lo + 1 < n ? t + 1 : T};
+  return sequence_of(cu, n, T, t, lo);
+}
+// a whole wave for one token: 64 offsets at once
+__device__ __forceinline__ Sequence sequence_of_wave(const int *cu, int n, int T, int t, int from, int lane) {
+  int lo = from < n ? from : n - 1, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const int before = __popcll(__ballot(at < hi && offset_at(cu, at < hi ? at : lo, T) <= t));
+    lo += (before > 1 ? before - 1 : 0) * step;
+    hi = hi < lo + step ? hi : lo + step;
+  }
+  const Sequence q = sequence_of([&](int s) { return offset_at(cu, s, T); }, n, T, t, lo);
+  return Sequence{__builtin_amdgcn_readfirstlane(q.seq), __builtin_amdgcn_readfirstlane(q.begin), __builtin_amdgcn_readfirstlane(q.end)};
 }
 
 }  // namespace gdn

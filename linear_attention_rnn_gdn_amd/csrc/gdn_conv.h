@@ -46,8 +46,16 @@ __device__ __forceinline__ typename Pack<T, VEC>::type narrow(const float (&x)[V
   else if constexpr (VEC == 8) p = to_bf16x8(x);
   else
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = x[i];
+    for (int i = 0; i < VEC; ++i) p[i] = (T)x[i];
   return p;
+}
+
+// A piece at a thread's byte offset from an address of the whole workgroup's.
+template <typename P> __device__ __forceinline__ P pick(const void *base, unsigned off) {
+  return *reinterpret_cast<const P *>(static_cast<const char *>(base) + off);
+}
+template <typename P> __device__ __forceinline__ void drop(void *base, unsigned off, const P &p) {
+  *reinterpret_cast<P *>(static_cast<char *>(base) + off) = p;
 }
 
 // A row of x or, where the token lies before its sequence, of the window;
@@ -60,17 +68,46 @@ __device__ __forceinline__ typename Pack<T, VEC>::type conv_row(const ConvArgs &
   return *reinterpret_cast<const P *>(static_cast<const T *>(a.h0) + ((size_t)seq * (W - 1) + (W - 1 + before)) * a.C + c);
 }
 
-constexpr int CONV_BATCH = 8, CONV_BWD_BATCH = 4;   // rows asked for at once
+// The weights of a workgroup's channels through LDS: they lie as [C][W], and a
+// thread's own VEC x W of them, read from memory, would be a line per thread
+// and load, many more than all the rest.
+template <int W, int VEC> struct Weights {
+  static constexpr int OWN = VEC * W, PITCH = OWN % 8 ? OWN : OWN + 4;   // (whole 16 bytes apart, not on the same banks)
+  float __attribute__((aligned(16))) lds[64 * PITCH];
+  __device__ __forceinline__ void stage(const ConvArgs &a, int first) {   // first channel
+    const int n = min(a.lanes * VEC, a.C - first) * W;
+    const float *w = a.weight + (size_t)first * W;
+    for (int i = threadIdx.x; i < n; i += 256) lds[i / OWN * PITCH + i % OWN] = w[i];
+  }
+  __device__ __forceinline__ void get(int l, float (&w)[W][VEC]) const {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][v] = lds[l * PITCH + v * W + k];
+  }
+};
+
+constexpr int CONV_OFFSETS = 255, CONV_ONES = 4;
+// Rows asked for at once, and again while these are worked on: whole windows,
+// which are rings then whose slots are known when the kernel is compiled.
+template <int W, int VEC> constexpr int conv_batch() { return (W == 3 ? 3 : 4) * (VEC == 1 ? CONV_ONES : 1); }
 
 template <int W, int VEC, typename T>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
+__global__ __launch_bounds__(256, 4) void conv_fwd_kernel(ConvArgs a) {
   using P = typename Pack<T, VEC>::type;
-  constexpr bool ROUGH = std::is_same<T, __bf16>::value;
+  constexpr int BATCH = conv_batch<W, VEC>();
   const int tid = threadIdx.x, tiles = (a.C / VEC + a.lanes - 1) / a.lanes;
   const int tile = blockIdx.x % tiles;
   const int64_t piece = blockIdx.x / tiles;
   const int c = (tile * a.lanes + (tid & (a.lanes - 1))) * VEC;
   const int rows = a.cu ? 1 : a.B;
+  __shared__ Weights<W, VEC> all;
+  __shared__ int offsets[CONV_OFFSETS + 1];   // of the first packed sequences (all of them, mostly)
+  all.stage(a, tile * a.lanes * VEC);
+  if (a.cu)
+    for (int i = tid; i <= min(a.B, CONV_OFFSETS); i += 256) offsets[i] = offset_at(a.cu, i, a.T);
+  __syncthreads();
+  auto offset = [&](int s) { return s <= CONV_OFFSETS ? offsets[s] : offset_at(a.cu, s, a.T); };
   if (c >= a.C) return;
   if (piece >= (int64_t)rows * a.runs) {   // the windows behind the sequences
     const int per = 256 >> a.lane_bits;
@@ -80,8 +117,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     int begin = 0, end = a.T;
     int64_t row = (int64_t)s * a.T;
     if (a.cu) {
-      begin = offset_at(a.cu, s, a.T);
-      end = max(begin, offset_at(a.cu, s + 1, a.T));
+      begin = offset(s);
+      end = max(begin, offset(s + 1));
       row = 0;
     }
     const int t = end - (W - 1) + j;
@@ -90,51 +127,71 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     return;
   }
   const int row = (int)(piece / a.runs);
-  const int64_t at = (int64_t)(piece % a.runs) * (256 >> a.lane_bits) * a.run + (int64_t)(tid >> a.lane_bits) * a.run;
+  const int64_t first = (piece % a.runs) * (256 >> a.lane_bits) * a.run, at = first + (tid >> a.lane_bits) * a.run;
   if (at >= a.T) return;
   const int t0 = (int)at, t1 = (int)min((int64_t)a.T, at + a.run);
   Sequence q{row, 0, a.T};
-  if (a.cu) q = sequence_at(a.cu, a.B, a.T, t0, 0);
   const T *x = static_cast<const T *>(a.x) + (int64_t)row * a.T * a.ld + c;
-  T *y = static_cast<T *>(a.y) + (int64_t)row * a.T * a.C + c;
-  float w[W][VEC], bias[VEC], win[W][VEC];
+  // rows from the workgroup's first token on, at 32-bit offsets of this thread's
+  const T *xb = static_cast<const T *>(a.x) + ((int64_t)row * a.T + first) * a.ld;
+  T *yb = static_cast<T *>(a.y) + ((int64_t)row * a.T + first) * a.C;
+  const unsigned step = (unsigned)(a.ld * sizeof(T)), last = (unsigned)(t1 - 1 - first) * step + c * (unsigned)sizeof(T);
+  unsigned xo = (unsigned)(t0 - first) * step + c * (unsigned)sizeof(T);
+  unsigned yo = ((unsigned)(t0 - first) * a.C + c) * (unsigned)sizeof(T);
+  float w[W][VEC], bias[VEC], win[W][VEC];   // token t's x: slot (t - t0) % W
+  all.get(tid & (a.lanes - 1), w);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    bias[i] = a.bias ? a.bias[c + i] : 0.f;
+  for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+  P in[BATCH], next[BATCH];
+  auto ask = [&](P(&in)[BATCH]) {   // the next tokens (past the run's last: that one)
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][i] = a.weight[(size_t)(c + i) * W + k];
-  }
+    for (int i = 0; i < BATCH; ++i) {
+      in[i] = pick<P>(xb, min(xo, last));
+      xo += step;
+    }
+  };
+  ask(in);
+  if (a.cu) q = sequence_at(offset, a.B, a.T, t0, 0);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) {
-    const int t = t0 - (W - 1) + k;
+  for (int k = 1; k < W; ++k) {
+    const int t = t0 + k - W;
     widen<VEC, T>(conv_row<W, VEC, T>(a, x + (int64_t)max(t, 0) * a.ld, q.seq, t - q.begin, c), win[k]);
   }
-  for (int tb = t0; tb < t1; tb += CONV_BATCH) {
-    P in[CONV_BATCH];
+  auto token = [&](int i) {
+    widen<VEC, T>(in[i], win[i % W]);
+    float o[VEC];
 #pragma unroll
-    for (int i = 0; i < CONV_BATCH; ++i) in[i] = *reinterpret_cast<const P *>(x + (int64_t)min(tb + i, t1 - 1) * a.ld);
+    for (int v = 0; v < VEC; ++v) {
+      float s = bias[v];
 #pragma unroll
-    for (int i = 0; i < CONV_BATCH; ++i) {
-      const int t = tb + i;
-      if (t >= t1) break;
-      if (t == q.end) {   // packed: the next sequence
-        q = sequence_at(a.cu, a.B, a.T, t, q.seq + 1);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) widen<VEC, T>(conv_row<W, VEC, T>(a, x, q.seq, k - (W - 1), c), win[k]);
-      }
-      widen<VEC, T>(in[i], win[W - 1]);
-      float o[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        float s = bias[v];
-#pragma unroll
-        for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-        o[v] = a.silu ? silu<ROUGH>(s) : s;
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
-      }
-      *reinterpret_cast<P *>(y + (int64_t)t * a.C) = narrow<VEC, T>(o);
+      for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[(i + 1 + k) % W][v], s);
+      o[v] = a.silu ? silu<true>(s) : s;
     }
+    drop<P>(yb, yo, narrow<VEC, T>(o));
+    yo += a.C * (unsigned)sizeof(T);
+  };
+  for (int tb = t0; tb < t1; tb += BATCH) {
+    ask(next);
+    // Nothing ends among them: mostly, and worth code of its own where a batch is
+    // a dozen tokens or so of one channel (61 MB packed, fp32: 17.8 us, 19.7
+    // without); of a pack it would take more registers than four waves have.
+    if (VEC == 1 && !__any(tb + BATCH > t1 || (q.end > t0 && q.end < tb + BATCH))) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) token(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (tb + i >= t1) break;
+        if (tb + i == q.end) {   // packed: the next sequence
+          q = sequence_at(offset, a.B, a.T, tb + i, q.seq + 1);
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) widen<VEC, T>(conv_row<W, VEC, T>(a, x, q.seq, k - (W - 1), c), win[(i + 1 + k) % W]);
+        }
+        token(i);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) in[i] = next[i];
   }
 }
 
@@ -162,7 +219,22 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) in[k] = *reinterpret_cast<const P *>(st + (size_t)k * a.C);
   in[W - 1] = *reinterpret_cast<const P *>(static_cast<const T *>(a.x) + b * a.ld + c);
-  float o[VEC];
+  float o[VEC], w[W][VEC];
+  // (a row's whole work is a few loads: its own weights in 16 bytes each, at once with the rest, beat a barrier)
+  const float *wp = a.weight + (size_t)c * W;
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][0] = wp[k];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC * W; i += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(wp + i);
+      w[i % W][i / W] = v.x;
+      w[(i + 1) % W][(i + 1) / W] = v.y;
+      w[(i + 2) % W][(i + 2) / W] = v.z;
+      w[(i + 3) % W][(i + 3) / W] = v.w;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < VEC; ++v) o[v] = a.bias ? a.bias[c + v] : 0.f;
 #pragma unroll
@@ -170,11 +242,11 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
     float x[VEC];
     widen<VEC, T>(in[k], x);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = fmaf(a.weight[(size_t)(c + v) * W + k], x[v], o[v]);
+    for (int v = 0; v < VEC; ++v) o[v] = fmaf(w[k][v], x[v], o[v]);
   }
   if (a.silu)
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = silu<std::is_same<T, __bf16>::value>(o[v]);
+    for (int v = 0; v < VEC; ++v) o[v] = silu<true>(o[v]);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) *reinterpret_cast<P *>(st + (size_t)k * a.C) = in[k + 1];
   *y = narrow<VEC, T>(o);
@@ -186,87 +258,104 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
 // need; the sums of weight and bias take its own tokens only.  They are summed
 // over the workgroup's runs in LDS and written as one piece per workgroup; a
 // second kernel adds the pieces in a fixed order.
+// Tokens go by W at a time, so that the windows of x and d are rings whose
+// slots are known when the kernel is compiled and nothing is moved; the rows of
+// the next W tokens are on their way meanwhile.
 template <int W, int VEC, typename T>
-__global__ __launch_bounds__(256, 2) void conv_bwd_kernel(ConvArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void conv_bwd_kernel(ConvArgs a) {
   using P = typename Pack<T, VEC>::type;
   __shared__ float red[256 * VEC];
   const int tid = threadIdx.x, tiles = (a.C / VEC + a.lanes - 1) / a.lanes;
   const int tile = blockIdx.x % tiles, piece = blockIdx.x / tiles;
   const int c = (tile * a.lanes + (tid & (a.lanes - 1))) * VEC, cc = min(c, a.C - VEC);   // (lanes past the last channel: its rows, not stored)
   const int row = piece / a.runs, per = 256 >> a.lane_bits;
-  const int64_t at = (int64_t)(piece % a.runs) * per * a.run + (int64_t)(tid >> a.lane_bits) * a.run;
+  const int64_t first = (int64_t)(piece % a.runs) * per * a.run, at = first + (tid >> a.lane_bits) * a.run;
   const bool on = c < a.C && (at < a.T || at == 0);   // (the first run also of an empty row: it writes dh0)
   float dw[W][VEC] = {}, db[VEC] = {};
+  __shared__ Weights<W, VEC> all;
+  all.stage(a, tile * a.lanes * VEC);
+  __syncthreads();
   if (on) {
-    const int t0 = (int)at, t1 = (int)min((int64_t)a.T, at + a.run), t2 = t1 + W - 1;
+    const int t0 = (int)at;
     const T *x = static_cast<const T *>(a.x) + (int64_t)row * a.T * a.ld + cc;
-    const T *dy = static_cast<const T *>(a.dy) + (int64_t)row * a.T * a.C + cc;
-    T *dx = static_cast<T *>(a.dx) + (int64_t)row * a.T * a.C + cc;
-    float w[W][VEC], bias[VEC], win[W][VEC], d[W][VEC] = {};   // d[k]: of token t - k
+    // rows from the workgroup's first token on, at 32-bit offsets of this thread's (none of an empty row)
+    const T *xb = static_cast<const T *>(a.x) + ((int64_t)row * a.T + first) * a.ld;
+    const T *db_ = static_cast<const T *>(a.dy) + ((int64_t)row * a.T + first) * a.C;
+    T *dxb = static_cast<T *>(a.dx) + ((int64_t)row * a.T + first) * a.C;
+    const unsigned e = sizeof(T), xs = (unsigned)a.ld * e, ys = (unsigned)a.C * e, co = cc * e;
+    const unsigned here = (unsigned)(t0 - first), left = (unsigned)min(a.T - 1 - t0, a.run + 2 * W);   // tokens behind t0 in the row
+    const unsigned xlast = (here + left) * xs + co, ylast = (here + left) * ys + co;
+    unsigned xo = here * xs + co, yo = here * ys + co, out = yo - (W - 1) * ys;
+    float w[W][VEC], bias[VEC], win[W][VEC], d[W][VEC] = {};   // token t's x and d: slot (t - t0) % W
+    all.get(tid & (a.lanes - 1), w);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      bias[i] = a.bias ? a.bias[cc + i] : 0.f;
+    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[cc + i] : 0.f;
+    P in[W], dd[W], in_next[W], dd_next[W];
+    auto ask = [&](P(&in)[W], P(&dd)[W]) {   // the next W tokens (past the last: that one)
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[k][i] = a.weight[(size_t)(cc + i) * W + k];
-    }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-      const int t = t0 - (W - 1) + k;
-      widen<VEC, T>(conv_row<W, VEC, T>(a, x + (int64_t)max(t, 0) * a.ld, row, t, cc), win[k]);
-    }
-    for (int tb = t0; tb < t2; tb += CONV_BWD_BATCH) {
-      P in[CONV_BWD_BATCH], dd[CONV_BWD_BATCH];
-#pragma unroll
-      for (int i = 0; i < CONV_BWD_BATCH; ++i) {
-        const int t = min(min(tb + i, t2 - 1), a.T - 1);
-        in[i] = t < 0 ? P{} : *reinterpret_cast<const P *>(x + (int64_t)t * a.ld);
-        dd[i] = t < 0 ? P{} : *reinterpret_cast<const P *>(dy + (int64_t)t * a.C);
+      for (int i = 0; i < W; ++i) {
+        in[i] = a.T ? pick<P>(xb, min(xo, xlast)) : P{};
+        dd[i] = a.T ? pick<P>(db_, min(yo, ylast)) : P{};
+        xo += xs;
+        yo += ys;
       }
+    };
+    ask(in, dd);
 #pragma unroll
-      for (int i = 0; i < CONV_BWD_BATCH; ++i) {
-        const int t = tb + i;
-        if (t >= t2) break;
+    for (int k = 1; k < W; ++k)
+      widen<VEC, T>(conv_row<W, VEC, T>(a, x + (int64_t)max(t0 + k - W, 0) * a.ld, row, t0 + k - W, cc), win[k]);
+    for (int r = 0; r <= a.run; r += W) {   // (run is a multiple of W: the last time the W - 1 tokens behind it)
+      if (t0 + r >= a.T + W - 1) break;
+      const bool own = r < a.run;
+      ask(in_next, dd_next);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
-#pragma unroll
-          for (int k = W - 1; k > 0; --k) d[k][v] = d[k - 1][v];
-        widen<VEC, T>(in[i], win[W - 1]);
-        widen<VEC, T>(dd[i], d[0]);
+      for (int i = 0; i < W; ++i) {
+        if (i == W - 1 && !own) break;
+        const int t = t0 + r + i;
+        widen<VEC, T>(in[i], win[i]);
+        widen<VEC, T>(dd[i], d[i]);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           if (a.silu) {
             float s = bias[v], y, g;
 #pragma unroll
-            for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-            silu_grad(s, y, g);
-            d[0][v] *= g;
+            for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[(i + 1 + k) % W][v], s);
+            silu_grad<true>(s, y, g);
+            d[i][v] *= g;
           }
-          if (t >= a.T) d[0][v] = 0.f;
-          if (t < t1) {
-            db[v] += d[0][v];
-#pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(d[0][v], win[k][v], dw[k][v]);
-          }
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
+          d[i][v] = t < a.T ? d[i][v] : 0.f;
         }
+        if (own)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            db[v] += d[i][v];
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(d[i][v], win[(i + 1 + k) % W][v], dw[k][v]);
+          }
         const int to = t - (W - 1);   // its gradient is complete
-        if (to < t0 && (t0 || !a.dh0)) continue;
+        const unsigned off = out;
+        out += ys;
+        if (r + i < W - 1 ? t0 || !a.dh0 : to >= a.T) continue;   // (an earlier run's, or none)
         float o[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           o[v] = 0.f;
 #pragma unroll
-          for (int k = 0; k < W; ++k) o[v] = fmaf(w[k][v], d[k][v], o[v]);
+          for (int k = 0; k < W; ++k) o[v] = fmaf(w[k][v], d[(i - k + W) % W][v], o[v]);
         }
         if (a.dh_T && to >= a.T - (W - 1)) {
-          float e[VEC];
-          widen<VEC, T>(*reinterpret_cast<const P *>(static_cast<const T *>(a.dh_T) + ((size_t)row * (W - 1) + to - a.T + W - 1) * a.C + cc), e);
+          float g[VEC];
+          widen<VEC, T>(*reinterpret_cast<const P *>(static_cast<const T *>(a.dh_T) + ((size_t)row * (W - 1) + to - a.T + W - 1) * a.C + cc), g);
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) o[v] += e[v];
+          for (int v = 0; v < VEC; ++v) o[v] += g[v];
         }
-        T *to_p = to < 0 ? static_cast<T *>(a.dh0) + ((size_t)row * (W - 1) + to + W - 1) * a.C + cc : dx + (int64_t)to * a.C;
-        *reinterpret_cast<P *>(to_p) = narrow<VEC, T>(o);
+        if (to < 0) *reinterpret_cast<P *>(static_cast<T *>(a.dh0) + ((size_t)row * (W - 1) + to + W - 1) * a.C + cc) = narrow<VEC, T>(o);
+        else drop<P>(dxb, off, narrow<VEC, T>(o));
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        in[i] = in_next[i];
+        dd[i] = dd_next[i];
       }
     }
   }

@@ -14,15 +14,16 @@ using namespace gdn;
 namespace {
 
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of 256 threads: a launch holds fewer than 2^32
-constexpr int kFwdRun = 16, kBwdRun = 32;         // tokens per thread
+constexpr int kMaxRow = 1 << 20;                  // elements from a token to the next (see lay_out)
+constexpr int kFwdRun = 16, kBwdRun = 64, kBwdShort = 16, kFewPieces = 512;   // tokens per thread
 
 int elem(const gdn_conv_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 
 gdn_status validate_conv(const gdn_conv_shape *s) {
   if (!s) return GDN_ERR_NULL;
   if (s->dtype != GDN_F32 && s->dtype != GDN_BF16) return GDN_ERR_DTYPE;
-  if (s->B < 1 || s->T < 0 || s->T > 1 << 30 || s->C < 1 || s->C > 1 << 24 || s->W < 2 || s->W > 4) return GDN_ERR_SHAPE;
-  if ((s->ld && s->ld < s->C) || (s->silu & ~1)) return GDN_ERR_SHAPE;
+  if (s->B < 1 || s->T < 0 || s->T > 1 << 30 || s->C < 1 || s->C > kMaxRow || s->W < 2 || s->W > 4) return GDN_ERR_SHAPE;
+  if ((s->ld && (s->ld < s->C || s->ld > kMaxRow)) || (s->silu & ~1)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 
@@ -48,16 +49,18 @@ ConvArgs conv_args(const gdn_conv_shape &s) {
   a.ld = s.ld ? s.ld : s.C;
   return a;
 }
-// 64 threads side by side in channels, fewer where there are fewer
-void lay_out(ConvArgs &a, int vec, int rows, int run) {
+// 64 threads side by side in channels, fewer where there are fewer, but so many
+// that a workgroup's tokens lie within 2^31 bytes: at 64, 4 runs of 64 tokens at
+// most, of 2^20 elements of 4 bytes.
+void lay_out(ConvArgs &a, int vec, int run, int elem) {
   const int groups = (a.C + vec - 1) / vec;
+  const int64_t ld = std::max<int64_t>(a.ld, a.C);
   a.lane_bits = 0;
-  while (a.lane_bits < 6 && (1 << a.lane_bits) < groups) ++a.lane_bits;
+  while (a.lane_bits < 6 && ((1 << a.lane_bits) < groups || ((int64_t)(256 >> a.lane_bits) * run + 16) * ld * elem >= 1ll << 31)) ++a.lane_bits;
   a.lanes = 1 << a.lane_bits;
   a.run = run;
   const int64_t per = (int64_t)(256 >> a.lane_bits) * run;
   a.runs = (int)((a.T + per - 1) / per);
-  (void)rows;
 }
 int tiles_of(const ConvArgs &a, int vec) { return (a.C / vec + a.lanes - 1) / a.lanes; }
 
@@ -68,6 +71,12 @@ gdn_status with_width(int W, F &&f) {
 template <typename F>
 gdn_status with_pack(const gdn_conv_shape &s, bool wide, F &&f) {
   if (s.dtype == GDN_BF16) return wide ? f(std::integral_constant<int, 8>{}, __bf16{}) : f(std::integral_constant<int, 1>{}, __bf16{});
+  return wide ? f(std::integral_constant<int, 4>{}, float{}) : f(std::integral_constant<int, 1>{}, float{});
+}
+
+template <typename F>
+gdn_status with_pack_bwd(const gdn_conv_shape &s, bool wide, F &&f) {
+  if (s.dtype == GDN_BF16) return wide ? f(std::integral_constant<int, 4>{}, __bf16{}) : f(std::integral_constant<int, 1>{}, __bf16{});
   return wide ? f(std::integral_constant<int, 4>{}, float{}) : f(std::integral_constant<int, 1>{}, float{});
 }
 
@@ -84,7 +93,7 @@ gdn_status conv_fwd(const gdn_conv_shape *s, bool packed, const int32_t *cu, con
   return with_pack(*s, wide(*s, {x, h0, y, h_T}), [&](auto vec, auto t) -> gdn_status {
     constexpr int VEC = decltype(vec)::value;
     using T = decltype(t);
-    lay_out(a, VEC, rows, kFwdRun);
+    lay_out(a, VEC, kFwdRun / s->W * s->W, sizeof(T));
     const int per = 256 >> a.lane_bits;
     const int64_t windows = h_T ? ((int64_t)s->B * (s->W - 1) + per - 1) / per : 0;
     const int64_t blocks = ((int64_t)rows * a.runs + windows) * tiles_of(a, VEC);
@@ -102,7 +111,10 @@ struct ConvPieces {
   size_t bytes;
 };
 ConvPieces pieces_of(const gdn_conv_shape &s, ConvArgs &a, int vec) {
-  lay_out(a, vec, s.B, kBwdRun);
+  for (int run = kBwdRun; run >= kBwdShort; run /= 2) {
+    lay_out(a, vec, run / s.W * s.W, elem(s));
+    if ((int64_t)s.B * a.runs * tiles_of(a, vec) >= kFewPieces) break;
+  }
   a.runs = std::max(a.runs, 1);   // (an empty row still writes dh0)
   const int64_t pieces = (int64_t)s.B * a.runs;
   return {pieces, align_up((size_t)pieces * (s.W + 1) * s.C * 4)};
@@ -130,7 +142,7 @@ gdn_status gdn_conv_step(const gdn_conv_shape *s, const void *x, const float *we
   GDN_TRY(aligned(*s, {x, state, y}, {weight, bias, slots}));
   ConvArgs a = conv_args(*s);
   a.x = x; a.weight = weight; a.bias = bias; a.slots = slots; a.state = state; a.y = y;
-  return with_pack(*s, wide(*s, {x, state, y}), [&](auto vec, auto t) -> gdn_status {
+  return with_pack(*s, wide(*s, {x, state, y, weight}), [&](auto vec, auto t) -> gdn_status {
     constexpr int VEC = decltype(vec)::value;
     using T = decltype(t);
     const int64_t blocks = (int64_t)s->B * ((s->C / VEC + 255) / 256);
@@ -148,7 +160,7 @@ gdn_status gdn_workspace_size_conv_bwd(const gdn_conv_shape *s, size_t *bytes) {
   GDN_TRY(validate_conv(s));
   // of the two layouts (16-byte pieces or single elements), the larger one
   ConvArgs a = conv_args(*s);
-  const size_t one = pieces_of(*s, a, 1).bytes, many = pieces_of(*s, a, s->dtype == GDN_BF16 ? 8 : 4).bytes;
+  const size_t one = pieces_of(*s, a, 1).bytes, many = pieces_of(*s, a, 4).bytes;
   *bytes = std::max(one, many);
   return GDN_OK;
 }
@@ -163,7 +175,7 @@ gdn_status gdn_conv_bwd(const gdn_conv_shape *s, const void *x, const float *wei
   a.x = x; a.weight = weight; a.bias = bias; a.h0 = h0; a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dh0 = dh0;
   a.part = static_cast<float *>(ws);
   hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
-  return with_pack(*s, wide(*s, {x, h0, dy, dh_T, dx, dh0}), [&](auto vec, auto t) -> gdn_status {
+  return with_pack_bwd(*s, wide(*s, {x, h0, dy, dh_T, dx, dh0}), [&](auto vec, auto t) -> gdn_status {
     constexpr int VEC = decltype(vec)::value;
     using T = decltype(t);
     const ConvPieces p = pieces_of(*s, a, VEC);

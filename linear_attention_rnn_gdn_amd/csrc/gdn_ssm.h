@@ -156,10 +156,7 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
   const int t0 = j * a.len, t1 = min(a.T, t0 + a.len);
   Sequence q{row, 0, a.T};
   auto next_sequence = [&](int t, int from) {
-    q = sequence_at(a.cu, a.B, a.T, t, from);
-    q.seq = __builtin_amdgcn_readfirstlane(q.seq);
-    q.begin = __builtin_amdgcn_readfirstlane(q.begin);
-    q.end = __builtin_amdgcn_readfirstlane(q.end);
+    q = sequence_of_wave(a.cu, a.B, a.T, t, from, lane);
   };
   if (a.cu) next_sequence(t0, 0);
   const int64_t r0 = (int64_t)row * a.T + t0;   // the segment's first token
@@ -402,7 +399,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
   *reinterpret_cast<float4 *>(p) = h;
   if (n0) return;
   if (a.D) s = fmaf(a.D[c], x, s);
-  if (a.z) s *= silu(to_f32(static_cast<const TI *>(a.z)[b * a.ld_z + c]));
+  if (a.z) s *= silu<std::is_same<TO, __bf16>::value>(to_f32(static_cast<const TI *>(a.z)[b * a.ld_z + c]));
   *y = from_f32<TO>(s);
 }
 
@@ -757,7 +754,7 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
         xs[i] = here && tl.on ? to_f32(xr[i]) : 0.f;
         const float g = here && tl.on ? to_f32(gr[i]) : 0.f;
         float sg, dsg;
-        silu_grad(to_f32(zr[i]), sg, dsg);
+        silu_grad<false>(to_f32(zr[i]), sg, dsg);
         ws[i] = g * dsg;
         gs[i] = gated ? g * sg : g;
       }
