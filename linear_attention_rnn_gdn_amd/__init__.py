@@ -40,6 +40,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -75,14 +76,6 @@ class GdnConvShape(ctypes.Structure):
 class GdnSsmShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "T", "C", "N", "G", "n_slots", "softplus", "ld_x", "ld_dt", "ld_z", "ld_b", "ld_c", "dtype", "o_dtype")]
-
-
-class GdnSsmInputs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias")]
-
-
-class GdnSsmGrads(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")]
 
 
 class GdnVerifyShape(ctypes.Structure):
@@ -171,7 +164,7 @@ def lib():
         L.gdn_linear_chunk_bwd.argtypes = [LP] + [P] * 13 + [SZ, P]
         L.gdn_linear_chunk_bwd.restype = I
         CP, MP, VP = (ctypes.POINTER(t) for t in (GdnConvShape, GdnSsmShape, GdnVerifyShape))
-        IP, GP = ctypes.POINTER(GdnSsmInputs), ctypes.POINTER(GdnSsmGrads)
+        IP = GP = ctypes.c_char_p   # gdn_ssm_inputs, gdn_ssm_grads: their pointers in a row
         for name, args in (("gdn_conv_fwd", [CP] + [P] * 7), ("gdn_conv_fwd_varlen", [CP] + [P] * 8),
                            ("gdn_conv_step", [CP] + [P] * 7), ("gdn_workspace_size_conv_bwd", [CP, ctypes.POINTER(SZ)]),
                            ("gdn_conv_bwd", [CP] + [P] * 11 + [SZ, P]),
@@ -856,6 +849,11 @@ def _columns(t, name, dtype, shape, dev, tail):
     if t.is_contiguous():
         return 0
     strides, width = t.stride(), 1
+    if len(shape) - tail == 1 and strides[-1] == 1 and (tail == 1 or strides[1] == shape[2]):   # (a step's, mostly)
+        width, ld = shape[1] if tail == 1 else shape[1] * shape[2], strides[0]
+        if width <= ld < 1 << 31:
+            return ld
+        width = 1
     for i in range(1, tail + 1):
         if strides[-i] != width and shape[-i] > 1:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
@@ -1053,10 +1051,13 @@ def _ssm_plan(kind, *sizes):
     return shape, int(n.value)
 
 
+_pack8, _pack9 = struct.Struct("8P").pack, struct.Struct("9P").pack
+
+
 def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, lead, others=()):
     """Checks the inputs of a scan or a step, and ``others`` as _check_tensors
     takes them; returns its sizes (channels, states, groups) and token strides,
-    and the C struct."""
+    and the pointers as gdn_ssm_inputs has them."""
     xs = _leading(x, "x", lead + 1)
     dev, ty, c = x.device, x.dtype, xs[-1]
     _dt(ty)
@@ -1072,8 +1073,8 @@ def _ssm_inputs(x, dt, A, B, C, D, z, dt_bias, lead, others=()):
     if dt_bias is not None:
         items.append((dt_bias, "dt_bias", torch.float32, (c,)))
     _check_tensors(dev, *items)
-    return (c, n, g), lds, GdnSsmInputs(x.data_ptr(), dt.data_ptr(), _addr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _addr(D),
-                                        _addr(dt_bias))
+    return (c, n, g), lds, _pack8(x.data_ptr(), dt.data_ptr(), 0 if z is None else z.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                  A.data_ptr(), 0 if D is None else D.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr())
 
 
 def _ssm_names(x, dt, A, B, C, D, z, dt_bias):
@@ -1159,7 +1160,8 @@ def ssm_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, h0=None, dh_T=None
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
         if out is None:
             out = {name: torch.empty(sh, dtype=t, device=dev) for name, (t, sh) in want.items()}
-        grads = GdnSsmGrads(**{name: _addr(out[name]) for name in want})
+        grads = _pack9(*[out[name].data_ptr() if name in want else 0
+                         for name in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")])
         _check(lib().gdn_ssm_bwd(shape, given, _addr(h0), _addr(dy), _addr(dh_T), grads, _addr(ws), ws.numel(), st),
                "gdn_ssm_bwd")
     return out

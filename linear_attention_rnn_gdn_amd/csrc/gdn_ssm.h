@@ -862,15 +862,44 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
   if (j == 0 && a.dh0) store_states<NS>(a.dh0 + sn, dh);
 }
 
-// dB and dC: the sums over a group's waves.  A wave takes one token and group,
-// 16 bytes of the 2 N values per lane, as many of the group's waves side by side
-// as that leaves room for.
+constexpr int SUM_AHEAD = 8;   // segments asked for at once
+// What is left to sum, in one launch.  The first workgroups: dA, dD and
+// ddt_bias over the segments, 64 channels of one of them each, four segments
+// side by side.  The others: dB and dC over a group's waves; a wave takes one
+// token and group, 16 bytes of the 2 N values per lane, as many of the group's
+// waves side by side as that leaves room for.
 template <int N, typename TI>
-__global__ __launch_bounds__(256) void ssm_bc_sum_kernel(SsmArgs a, TI *dB, TI *dC, int64_t tokens) {
+__global__ __launch_bounds__(256) void ssm_sum_kernel(SsmArgs a, float *dA, float *dD, float *dbias, TI *dB, TI *dC, int64_t tokens) {
   constexpr int L = 2 * N / 4, R = 64 / L;   // lanes per row of values, rows at once
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane % L * 4;
-  const int64_t i = (int64_t)blockIdx.x * 4 + wave, t = i / a.G;
-  const int g = (int)(i % a.G);
+  __shared__ double red[4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tiles = (a.C + 63) / 64;
+  const int64_t rest = (int64_t)blockIdx.x - (N + 2) * (int64_t)tiles;
+  if (rest < 0) {
+    const int n = blockIdx.x / tiles, c = blockIdx.x % tiles * 64 + lane;
+    const int64_t units = (int64_t)a.rows * a.J, step = (int64_t)(N + 2) * a.C;
+    const float *p = a.part_a + (int64_t)n * a.C + min(c, a.C - 1);
+    double s = 0.;
+    for (int64_t u = wave; u < units; u += 4 * SUM_AHEAD) {
+      float v[SUM_AHEAD];
+#pragma unroll
+      for (int i = 0; i < SUM_AHEAD; ++i) v[i] = p[min(u + 4 * i, units - 1) * step];
+#pragma unroll
+      for (int i = 0; i < SUM_AHEAD; ++i) s += u + 4 * i < units ? (double)v[i] : 0.;
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave || c >= a.C) return;
+    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (n < N) dA[(size_t)c * N + n] = (float)s;
+    else if (n == N) {
+      if (dD) dD[c] = (float)s;
+    } else if (dbias) {
+      dbias[c] = (float)s;
+    }
+    return;
+  }
+  const int64_t i = rest * 4 + wave, t = i / a.G;
+  const int g = (int)(i % a.G), n = lane % L * 4;
   if (t >= tokens) return;
   const float *p = a.part_bc + (t * a.tiles + g * a.per) * 2 * N + n;
   float4 s{0.f, 0.f, 0.f, 0.f};
@@ -886,30 +915,6 @@ __global__ __launch_bounds__(256) void ssm_bc_sum_kernel(SsmArgs a, TI *dB, TI *
   TI *to = (n < N ? dB : dC) + (t * a.G + g) * N + n % N;
   if constexpr (std::is_same<TI, float>::value) *reinterpret_cast<float4 *>(to) = s;
   else *reinterpret_cast<uint2 *>(to) = uint2{pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
-}
-
-// dA, dD and ddt_bias: the sums over the segments, 64 channels of one of them
-// per workgroup, 16 segments side by side.
-template <int N>
-__global__ __launch_bounds__(1024) void ssm_a_sum_kernel(SsmArgs a, float *dA, float *dD, float *dbias) {
-  __shared__ double red[16][64];
-  const int lane = threadIdx.x & 63, r = threadIdx.x >> 6, tiles = (a.C + 63) / 64;
-  const int n = blockIdx.x / tiles, c = blockIdx.x % tiles * 64 + lane;
-  const int64_t units = (int64_t)a.rows * a.J;
-  double s = 0.;
-  if (c < a.C)
-    for (int64_t u = r; u < units; u += 16) s += (double)a.part_a[((size_t)u * (N + 2) + n) * a.C + c];
-  red[r][lane] = s;
-  __syncthreads();
-  if (r || c >= a.C) return;
-#pragma unroll
-  for (int i = 1; i < 16; ++i) s += red[i][lane];
-  if (n < N) dA[(size_t)c * N + n] = (float)s;
-  else if (n == N) {
-    if (dD) dD[c] = (float)s;
-  } else if (dbias) {
-    dbias[c] = (float)s;
-  }
 }
 
 }  // namespace gdn

@@ -104,7 +104,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   return l;
 }
 gdn_status check_sizes(const gdn_ssm_shape &s, const SsmArgs &a, const Layout &l) {
-  if (((int64_t)a.rows * l.J + s.B) * a.tiles > kMaxWaves) return GDN_ERR_SHAPE;
+  if (((int64_t)a.rows * l.J + s.B) * a.tiles * (s.N > 16 ? 2 : 1) > kMaxWaves) return GDN_ERR_SHAPE;
   if ((int64_t)a.rows * a.tiles * s.N > kMaxWaves / 8) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
@@ -234,13 +234,9 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *s, const gdn_ssm_inputs *in, const f
       }
       hipLaunchKernelGGL((ssm_bwd_kernel<N, TI>), dim3(walks), dim3(64 * SsmBwd<N>::WAVES), 0, st, a);
       GDN_TRY(check_launch());
-      if (tokens) {
-        hipLaunchKernelGGL((ssm_bc_sum_kernel<N, TI>), dim3((unsigned)bc), dim3(256), 0, st, a, static_cast<TI *>(out->dB),
-                           static_cast<TI *>(out->dC), tokens);
-        GDN_TRY(check_launch());
-      }
-      hipLaunchKernelGGL(ssm_a_sum_kernel<N>, dim3((unsigned)((N + 2) * ((s->C + 63) / 64))), dim3(1024), 0, st, a, out->dA, out->dD,
-                         out->ddt_bias);
+      const int64_t sums = (int64_t)(N + 2) * ((s->C + 63) / 64) + bc;
+      hipLaunchKernelGGL((ssm_sum_kernel<N, TI>), dim3((unsigned)sums), dim3(256), 0, st, a, out->dA, out->dD, out->ddt_bias,
+                         static_cast<TI *>(out->dB), static_cast<TI *>(out->dC), tokens);
       return check_launch();
     };
     return s->dtype == GDN_BF16 ? run(__bf16{}) : run(float{});
