@@ -38,6 +38,8 @@ struct SsmArgs {
   float *end, *sum, *in;        // [rows, J, tiles, N, 64], [rows, J, tiles, 64]: folded segments; states entering them
   int *fresh;                   // [rows, J]: a sequence begins in the segment
   float *rend, *rin;            // the same of the states' cotangents, from the last token to the first
+  float *mark, *mark_sum;       // gradients: [rows, J, marks, tiles, N, 64], [rows, J, marks, tiles, 64]: the folded state within
+  int marks;                    // a segment in front of each piece of the way back but the first, and the sum of d up to there
   float *part_bc, *part_a;      // gradients: [tokens, tiles, 2 N], [rows, J, N + 2, C]
 };
 
@@ -65,14 +67,6 @@ template <int N, typename TI> struct Row {
   // is for all of them: what is asked for next has to be asked for behind it.
   __device__ __forceinline__ void wait() const { asm volatile("" ::"s"(w[0]), "s"(w[WORDS - 1])); }
 };
-template <int N, typename TI>
-__device__ __forceinline__ void load_row(const TI *p, float (&x)[N]) {
-  Row<N, TI> r;
-  r.load(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = r.at(i);
-}
-
 // An element at a lane's byte offset from a row that is the same for the whole
 // wave: one scalar address per row, and one 32-bit register for all rows.
 template <typename T>
@@ -412,7 +406,13 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
 //   du = sum_n B_n dh_n,  dd = x du + sum_n A_n g_n,  dx = d du + D ds,  ddt = dd softplus'.
 // Folding a segment needs one pass in token order for both directions: with P
 // the product of the decays so far, the cotangent that leaves the segment at
-// its front is sum_t P_t C_t ds_t.
+// its front is sum_t P_t C_t ds_t.  The states that it passes in front of the
+// pieces that the way back takes are noted: with the segment's incoming state
+// decayed up to there they are the states themselves.
+template <int N> struct SsmBwd {
+  static constexpr int NS = N < 16 ? N : 16, WAVES = N / NS, S = NS == 8 ? 8 : 4;   // states and waves per channel, tokens per piece
+};
+
 template <int N, typename TI>
 __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
   using R = Row<N, TI>;
@@ -469,6 +469,12 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
   }
   for (int k = 0; k < len; k += SSM_BATCH) {
     if (k + SSM_BATCH < len) ask(k + SSM_BATCH, next);
+    if (k && k % SsmBwd<N>::S == 0) {
+      const size_t m = ((size_t)unit * a.marks + k / SsmBwd<N>::S - 1) * a.tiles + tile;
+      a.mark_sum[m * 64 + lane] = sum;
+#pragma unroll
+      for (int n = 0; n < N; ++n) a.mark[(m * N + n) * 64 + lane] = h[n];
+    }
     float d[SSM_BATCH], u[SSM_BATCH], g[SSM_BATCH];
 #pragma unroll
     for (int i = 0; i < SSM_BATCH; ++i) {   // (a token past the last: no step, no cotangent)
@@ -581,12 +587,12 @@ __device__ __forceinline__ int reduced_index(int lane) {
 template <int M> __device__ __forceinline__ bool reduced_writer(int lane) { return (lane & (64 / M - 1)) == 0; }
 
 // The way back over a segment takes pieces of S tokens, whose states a lane
-// holds in registers.  The states at every MARK-th token and the segment's
-// steps d stay in LDS from a first pass in token order; a piece that does not
-// begin at a mark walks to its front again.  (8 waves per compute unit have
-// 20 KB each; marks at every piece would take twice that and leave 5.)  Of 32
-// states a wave takes 16, and the two waves of a channel exchange their sums
-// over states once per piece.
+// holds in registers, from the state that the fold noted in front of each.  Of
+// 32 states a wave takes 16, and the two waves of a channel exchange their sums
+// over states once per piece.  A piece's noted state is asked for while the
+// piece behind it is worked on: at 4096 tokens of 4096 channels with 16 states
+// this kernel takes 300 us so, and 422 where it asks for what it needs at once.
+// (Asking for the tokens' elements ahead too spills, and gained nothing.)
 //
 // A lane's registers stay below 256, two waves per SIMD: with more, copies of
 // live values to accumulation registers are placed where paths join, and this
@@ -595,23 +601,17 @@ template <int M> __device__ __forceinline__ bool reduced_writer(int lane) { retu
 // lost).  So there is room for no more tokens, tokens are fenced from each
 // other, and what differs between calls (a gate or none) branches on scalars,
 // never on lanes.
-template <int N> struct SsmBwd {
-  static constexpr int NS = N < 16 ? N : 16, WAVES = N / NS, S = NS == 8 ? 8 : 4, MARK = 8, LEN = 32;
-};
-
 template <int N, typename TI>
 __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmArgs a) {
   using K = SsmBwd<N>;
   using R = Row<K::NS, TI>;
-  constexpr int S = K::S, NS = K::NS, LEN = K::LEN;
-  __shared__ float marks[K::WAVES][LEN / K::MARK - 1][NS][64];
-  __shared__ float steps[K::WAVES][LEN][64];
+  constexpr int S = K::S, NS = K::NS;
   __shared__ float sums[K::WAVES][S][3][K::WAVES > 1 ? 64 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile = blockIdx.x % a.tiles;
   const int64_t unit = blockIdx.x / a.tiles;
   const Tile tl = tile_of(a, tile, lane);
   const int c = tl.c, row = (int)(unit / a.J), j = (int)(unit % a.J), n0 = wave * NS;
-  const int t0 = j * a.len, len = min(a.T - t0, a.len);   // (LEN at most, whole marks)
+  const int t0 = j * a.len, len = min(a.T - t0, a.len);
   const int64_t r0 = (int64_t)row * a.T + t0;            // the segment's first token
   const bool gated = a.z != nullptr;                      // (without a gate x stands in for z, and is not used)
   const int64_t ld_z = gated ? a.ld_z : a.ld_x;
@@ -624,20 +624,16 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
   const size_t v = (size_t)unit * a.tiles + tile, vn = (v * N + n0) * 64 + lane, sn = ((size_t)row * a.C + c) * N + n0;
   const unsigned ci = c * sizeof(TI), cr = reduced_index<NS>(lane) * 4;
-  float(*mark)[NS][64] = marks[wave];
-  float(*step)[64] = steps[wave];
-  float A[NS], h[NS], dh[NS], dA[NS];
+  float A[NS], h[NS], dh[NS], dA[NS];   // h: the state in front of the segment
   load_states<NS>(a.A + (size_t)c * N + n0, A);
-  auto front = [&]() {
-    if (j > 0)
+  if (j > 0)
 #pragma unroll
-      for (int n = 0; n < NS; ++n) h[n] = a.in[vn + n * 64];
-    else if (a.h0)
-      load_states<NS>(a.h0 + sn, h);
-    else
+    for (int n = 0; n < NS; ++n) h[n] = a.in[vn + n * 64];
+  else if (a.h0)
+    load_states<NS>(a.h0 + sn, h);
+  else
 #pragma unroll
-      for (int n = 0; n < NS; ++n) h[n] = 0.f;
-  };
+    for (int n = 0; n < NS; ++n) h[n] = 0.f;
   if (j + 1 < a.J)
 #pragma unroll
     for (int n = 0; n < NS; ++n) dh[n] = a.rin[vn + n * 64];
@@ -658,55 +654,15 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * A[n]), h[n], u * B.at(n));
   };
-  // In token order: every step, and the states at the marks.  What comes next
-  // is asked for one batch (of x and dt) or token (of B) ahead.
-  {
-    constexpr int Q = SSM_BATCH;
-    TI xs[Q], ds[Q], xn[Q], dn[Q];
-    auto ask = [&](int k, TI(&xs)[Q], TI(&ds)[Q]) {
-      const unsigned off = fresh_offset(ci);
+  float front[NS], front_sum = 0.f;
+  auto ask_front = [&](int k) {
+    if (k <= 0) return;
+    const size_t m = ((size_t)unit * a.marks + k / S - 1) * a.tiles + tile;
+    front_sum = a.mark_sum[m * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        const int64_t at = max(min(k + i, len - 1), 0);
-        xs[i] = raw(x + at * a.ld_x, off);
-        ds[i] = raw(dt + at * a.ld_dt, off);
-      }
-    };
-    R B, Bn;
-    if (len > 0) {
-      ask(0, xs, ds);
-      B.load(Bm);
-    }
-    front();
-    for (int k = 0; k < len; k += Q) {
-      if (k + Q < len) ask(k + Q, xn, dn);
-      float d[Q];
-#pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        d[i] = step_size(a, to_f32(ds[i]) + bias);
-        step[k + i][lane] = d[i];   // (past the last token: its step again, not used)
-      }
-      if (k && k % K::MARK == 0)
-#pragma unroll
-        for (int n = 0; n < NS; ++n) mark[k / K::MARK - 1][n][lane] = h[n];
-      if (k / K::MARK < (len - 1) / K::MARK) {   // (nobody starts behind the last mark)
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-          B.wait();
-          __builtin_amdgcn_sched_barrier(0);
-          Bn.load(Bm + (int64_t)min(k + i + 1, len - 1) * a.ld_b);
-          __builtin_amdgcn_sched_barrier(0);
-          advance(d[i], to_f32(xs[i]), B, h);
-          B = Bn;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        xs[i] = xn[i];
-        ds[i] = dn[i];
-      }
-    }
-  }
+    for (int n = 0; n < NS; ++n) front[n] = a.mark[(m * N + n0 + n) * 64 + lane];
+  };
+  ask_front((len - 1) / S * S);
   for (int k = (len - 1) / S * S; k >= 0 && len > 0; k -= S) {
     // per token: x, the step, its slope, the cotangent of s, and what s is multiplied with in dz
     float xs[S], ds[S], slope[S], gs[S], ws[S], hs[S + 1][NS];
@@ -723,34 +679,19 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
         gr[i] = raw(dy + at * a.C, off);
         zr[i] = raw(z + at * ld_z, off);
       }
-      // the state at the piece's front
-      const int m = k / K::MARK;
-      if (m) {
+      // the state in front of the piece (the fold began the row's first segment with h0 itself)
 #pragma unroll
-        for (int n = 0; n < NS; ++n) hs[0][n] = mark[m - 1][n][lane];
-      } else {
-        front();
-#pragma unroll
-        for (int n = 0; n < NS; ++n) hs[0][n] = h[n];
+      for (int n = 0; n < NS; ++n) {
+        hs[0][n] = k ? front[n] : 0.f;
+        if (j > 0 || k == 0) hs[0][n] = fmaf(__builtin_amdgcn_exp2f(k ? front_sum * A[n] : 0.f), h[n], hs[0][n]);
       }
-      if constexpr (S < K::MARK) {
-        if (k % K::MARK) {   // S tokens behind the mark
-          TI xm[S];
-#pragma unroll
-          for (int i = 0; i < S; ++i) xm[i] = raw(x + (int64_t)(k - S + i) * a.ld_x, off);
-#pragma unroll
-          for (int i = 0; i < S; ++i) {
-            R B;
-            B.load(Bm + (int64_t)(k - S + i) * a.ld_b);
-            advance(step[k - S + i][lane], to_f32(xm[i]), B, hs[0]);
-          }
-        }
-      }
+      ask_front(k - S);
 #pragma unroll
       for (int i = 0; i < S; ++i) {   // a token past the last, or a lane past the last channel: no step, no cotangent
         const bool here = k + i < len;
-        slope[i] = a.softplus ? sigmoid(to_f32(dr[i]) + bias) : 1.f;
-        ds[i] = here ? step[min(k + i, LEN - 1)][lane] : 0.f;
+        const float v = to_f32(dr[i]) + bias;
+        slope[i] = a.softplus ? sigmoid(v) : 1.f;
+        ds[i] = here ? step_size(a, v) : 0.f;
         xs[i] = here && tl.on ? to_f32(xr[i]) : 0.f;
         const float g = here && tl.on ? to_f32(gr[i]) : 0.f;
         float sg, dsg;

@@ -14,7 +14,27 @@ using namespace gdn;
 namespace {
 
 constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 threads
-constexpr int kWaves = 4096, kShortest = 16, kFew = 1536, kFewest = 128;
+// Segments of a forward pass: as many as give 4096 walks, four per SIMD.  At
+// 4096 tokens of 4096 channels with 16 states, and at 5 packed sequences of
+// 2688 channels, 1024 walks took 364 and 425 us, 2048 190 and 235, 4096 144 and
+// 179, 8192 154 and 188 (a segment more costs its state's two passes).
+constexpr int kWaves = 4096;
+// ... of 16 tokens or more: 8, 16, 32 and 64 took 26, 27, 36 and 60 us at 512
+// tokens of 512 channels, 48, 38, 40 and 62 at 2048 tokens of them, and 106 and
+// 66 (8 and 16) at 8192 tokens of 64.
+constexpr int kShortest = 16;
+// Segments of the gradients have 8, 16, 32 or 64 tokens, by the waves that 32
+// would give: fewer than 256, than 1536, than 8192, or more.  Measured, in us:
+//   waves of 32 tokens (T x C)      8     16     32     64
+//      128   (512 x 512)           41     46     73    131
+//      512   (2048 x 512)          72     64     83    139
+//     1344   (2048 x 1344)        131    110    116    152
+//     2048   (2048 x 2048)        170    140    122    155
+//     4096   (2048 x 4096)        333    258    228    232
+//     7168   (4096 x 3584)        584    441    387    393
+//     8192   (8192 x 2048)        720    513    448    413
+// (Short ones fill the chip, long ones need fewer passes over a state.)
+constexpr int kFewest = 256, kFew = 1536, kMany = 8192;
 
 int elem(const gdn_ssm_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 int64_t ld(int32_t given, int64_t dense) { return given ? given : dense; }
@@ -64,15 +84,17 @@ gdn_status with_types(const gdn_ssm_shape &s, F &&f) {
 
 // Tokens per segment, segments per row, and where the workspace's pieces lie.
 struct Layout {
-  int len, J;
-  size_t end, in, sum, fresh, rend, rin, part_bc, part_a, total;
+  int len, J, marks;
+  size_t end, in, sum, fresh, rend, rin, mark, mark_sum, part_bc, part_a, total;
 };
 Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   Layout l{};
   if (grads) {
-    const int64_t pieces = (int64_t)a.rows * a.tiles * ((s.T + 31) / 32);
-    l.len = pieces < kFewest ? 8 : pieces < kFew ? 16 : 32;
+    const int64_t waves = (int64_t)a.rows * a.tiles * ((s.T + 31) / 32) * (s.N > 16 ? 2 : 1);
+    l.len = waves < kFewest ? 8 : waves < kFew ? 16 : waves < kMany ? 32 : 64;
     l.J = std::max(1, (s.T + l.len - 1) / l.len);
+    const int piece = s.N == 8 ? SsmBwd<8>::S : SsmBwd<16>::S;
+    l.marks = l.len / piece - 1;
   } else {
     const int64_t walks = (int64_t)a.rows * a.tiles, want = std::max<int64_t>(1, kWaves / walks);
     const int64_t len = (s.T + want - 1) / want;
@@ -86,7 +108,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
     return at;
   };
   const size_t units = (size_t)a.rows * l.J, states = units * a.tiles * s.N * 64 * 4;
-  if (l.J > 1) {
+  if (l.J > 1 || grads) {
     l.end = take(states);
     l.in = take(states);
     l.sum = take(units * a.tiles * 64 * 4);
@@ -97,6 +119,8 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
     }
   }
   if (grads) {
+    l.mark = take(states * l.marks);
+    l.mark_sum = take(units * l.marks * a.tiles * 64 * 4);
     l.part_bc = take((size_t)s.B * s.T * a.tiles * 2 * s.N * 4);
     l.part_a = take(units * (s.N + 2) * s.C * 4);
   }
@@ -110,7 +134,8 @@ gdn_status check_sizes(const gdn_ssm_shape &s, const SsmArgs &a, const Layout &l
 }
 void place(SsmArgs &a, const Layout &l, void *ws) {
   char *p = static_cast<char *>(ws);
-  a.len = l.len; a.J = l.J;
+  a.len = l.len; a.J = l.J; a.marks = l.marks;
+  a.mark = reinterpret_cast<float *>(p + l.mark); a.mark_sum = reinterpret_cast<float *>(p + l.mark_sum);
   a.end = reinterpret_cast<float *>(p + l.end); a.in = reinterpret_cast<float *>(p + l.in);
   a.sum = reinterpret_cast<float *>(p + l.sum); a.fresh = reinterpret_cast<int *>(p + l.fresh);
   a.rend = reinterpret_cast<float *>(p + l.rend); a.rin = reinterpret_cast<float *>(p + l.rin);
@@ -226,9 +251,11 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *s, const gdn_ssm_inputs *in, const f
     constexpr int N = decltype(n)::value;
     auto run = [&](auto ti) -> gdn_status {
       using TI = decltype(ti);
-      if (l.J > 1) {
+      if (s->T > SsmBwd<N>::S) {   // (one piece needs no marks)
         hipLaunchKernelGGL((ssm_bwd_fold_kernel<N, TI>), dim3(walks), dim3(64), 0, st, a);
         GDN_TRY(check_launch());
+      }
+      if (l.J > 1) {
         hipLaunchKernelGGL(ssm_scan_kernel<N>, dim3(2 * scan_blocks(a)), dim3(256), 0, st, a);
         GDN_TRY(check_launch());
       }
