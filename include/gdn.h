@@ -502,7 +502,7 @@ gdn_status gdn_linear_chunk_bwd(const gdn_linear_shape *shape, const void *q, co
  *            gradients are fp32
  * Pointers have to be aligned to an element only; rows that are whole 16-byte
  * pieces (C and ld multiples of 16 bytes, pointers 16-byte aligned) are faster.
- * Sums are fp32, rounded once.  C, ld <= 2^20, T <= 2^30, and a launch has to
+ * Sums are fp32, rounded once.  B <= 2^24, C, ld <= 2^20, T <= 2^30, and a launch has to
  * stay below 2^32 threads (GDN_ERR_SHAPE). */
 typedef struct {
   int32_t B, T, C, W, ld, n_slots, silu, dtype;
@@ -601,7 +601,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, co
 
 /* The gradients of L = sum <y, dy> + <h_T, dh_T>: dy [B, T, C] dtype; dh_T
  * [B, C, N] fp32 or NULL (zero); o_dtype is not used.  Sums over tokens and
- * channels are made in a fixed order. */
+ * channels are made in a fixed order.  The workspace holds the state in front
+ * of every 4th token (N = 8: every 8th). */
 gdn_status gdn_ssm_bwd(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, const float *h0,
                        const void *dy, const float *dh_T, const gdn_ssm_grads *out, void *ws,
                        size_t ws_bytes, void *hip_stream);

@@ -89,6 +89,7 @@ struct Layout {
 };
 Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   Layout l{};
+  if ((int64_t)a.rows * a.tiles > kMaxWaves) return l;   // (refused by check_sizes: the products below would not fit)
   if (grads) {
     const int64_t waves = (int64_t)a.rows * a.tiles * ((s.T + 31) / 32) * (s.N > 16 ? 2 : 1);
     l.len = waves < kFewest ? 8 : waves < kFew ? 16 : waves < kMany ? 32 : 64;
@@ -99,7 +100,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
     const int64_t walks = (int64_t)a.rows * a.tiles, want = std::max<int64_t>(1, kWaves / walks);
     const int64_t len = (s.T + want - 1) / want;
     l.len = (int)std::max<int64_t>(kShortest, (len + SSM_BATCH - 1) / SSM_BATCH * SSM_BATCH);
-    l.J = (s.T + l.len - 1) / l.len;
+    l.J = (int)(((int64_t)s.T + l.len - 1) / l.len);
   }
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -128,6 +129,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   return l;
 }
 gdn_status check_sizes(const gdn_ssm_shape &s, const SsmArgs &a, const Layout &l) {
+  if ((int64_t)a.rows * a.tiles > kMaxWaves) return GDN_ERR_SHAPE;
   if (((int64_t)a.rows * l.J + s.B) * a.tiles * (s.N > 16 ? 2 : 1) > kMaxWaves) return GDN_ERR_SHAPE;
   if ((int64_t)a.rows * a.tiles * s.N > kMaxWaves / 8) return GDN_ERR_SHAPE;
   return GDN_OK;

@@ -8,8 +8,8 @@ with fewer than 8 roundings of its value; its derivative, with slope at most
 0.5, likewise.  So |y| is off by at most 2^-24 (1.1 (W + 2) P + 8 |y|), d = dy
 act' by |dy| 2^-24 (0.5 (W + 2) P + 10), a gradient by the sum of those errors
 over its terms and (terms + 2) 2^-24 of the terms' sizes; a sum over tokens is
-made of runs of 32, up to 256 of them, and pieces in fp64: 32 + 256 roundings at
-most.  Outputs in bf16 are rounded once more, by at most half a step, 2^-8 of
+made of runs of at most 64, up to 64 of them where there are that many tokens,
+and pieces in fp64: fewer than 300 roundings.  Outputs in bf16 are rounded once more, by at most half a step, 2^-8 of
 the value.
 """
 import numpy as np
