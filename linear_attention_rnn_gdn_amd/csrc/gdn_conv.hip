@@ -16,7 +16,7 @@ namespace {
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of 256 threads: a launch holds fewer than 2^32
 constexpr int kMaxRow = 1 << 20;                  // elements from a token to the next (see lay_out)
 // Tokens per thread, rounded down to whole windows.  Forward: at 4096 tokens of
-// 4096 channels in bf16 8 took 33 us (each thread reads its W - 1 tokens of
+// 8192 channels in bf16 8 took 33 us (each thread reads its W - 1 tokens of
 // window too), 16 30 and 32 32.4 (too few waves).
 constexpr int kFwdRun = 16;
 // Gradients: 16, 32 and 64 took 60.6, 58.7 and 53 us there (a workgroup's sums

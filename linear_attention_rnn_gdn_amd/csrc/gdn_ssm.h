@@ -14,6 +14,11 @@
 // zero, or from the sequence's own state if it begins there) and the sum of d,
 // a second carries the states from segment to segment (the decay of a whole
 // segment is e^{A sum d}), and the walks start from those.
+// Measured at 4096 tokens of 4096 channels with 16 states in bf16 (vector ALU
+// busy; its instructions per token and wave): forward 138 us = folds 59 (89%;
+// 89) + scan 12 + walks 80 (88%; 123), of which 5 N are the recurrence's own;
+// gradients 401 us = folds 104 (86%; 153) + scan 19 + walks 300 (81%; 449) +
+// sums 11.  One token of 256 rows with 4096 channels: 28 us, 143 MB, 5.0 TB/s.
 #pragma once
 #include <type_traits>
 
@@ -116,7 +121,9 @@ __device__ __forceinline__ void store_states(float *p, const float (&h)[N]) {
 
 __device__ __forceinline__ float step_size(const SsmArgs &a, float v) { return a.softplus ? softplus(v, exp_neg_abs(v)) : v; }
 
-constexpr int SSM_BATCH = 4;   // tokens asked for at once, and worked on without a branch between them
+// Tokens asked for at once, and worked on without a branch between them (8 in the walk took 140 us instead of
+// 144; the fold for the gradients notes states between batches, at every 4th or 8th token).
+constexpr int SSM_BATCH = 4;
 
 // One wave: 64 channels of one segment.  FOLD: only the segment's end state
 // and sum of d.  The elements of the next SSM_BATCH tokens are on their way
@@ -296,6 +303,7 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
 // state): its four waves fold a quarter of the segments each, exchange what
 // they folded and go over them again from what enters their quarter.  Segment
 // j's own state is complete where a sequence begins in it.
+// (The scan moves two states per segment, 33 MB in 12 us at 64 segments of 4096 channels; latency bounds it.)
 constexpr int SCAN_AHEAD = 16;   // segments asked for at once
 template <int N>
 __global__ __launch_bounds__(256) void ssm_scan_kernel(SsmArgs a) {

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 threads
 // Segments of a forward pass: as many as give 4096 walks, four per SIMD.  At
-// 4096 tokens of 4096 channels with 16 states, and at 5 packed sequences of
-// 2688 channels, 1024 walks took 364 and 425 us, 2048 190 and 235, 4096 144 and
+// 4096 tokens of 4096 channels with 16 states, and at 12 packed sequences (9925
+// tokens) of 2000 channels, 1024 walks took 364 and 425 us, 2048 190 and 235, 4096 144 and
 // 179, 8192 154 and 188 (a segment more costs its state's two passes).
 constexpr int kWaves = 4096;
 // ... of 16 tokens or more: 8, 16, 32 and 64 took 26, 27, 36 and 60 us at 512

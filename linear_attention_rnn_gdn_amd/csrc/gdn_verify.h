@@ -12,8 +12,8 @@
 // Where no child is accepted, or there is none, the next token is drawn from
 // what is left of p: the lowest v whose running sum passes u times the whole.
 //
-// Unscaled, the residual after k refusals is max(p - t q, 0) with one number
-// t: clamping at zero before taking off more changes nothing, so
+// Unscaled, the residual after k refusals is max(p - t q, 0) with one number t:
+// clamping at zero before taking off more changes nothing, so
 //   r_k = max(p - t_k q, 0),  t_k = s_0 + .. + s_{k-1},  s_0 = 1,  s_k = sum r_k
 // and a child is accepted if  u s_k q(x) < r_k(x).  A refusal before a further
 // child costs one pass over the vocabulary for s_k; all else are reads of
@@ -22,6 +22,12 @@
 // Children have higher numbers than their parent, so one sweep over the nodes
 // in order finds the path.  All comparisons and sums are in fp64 of the fp32
 // inputs: they decide tokens.
+//
+// Rows are few, so the vocabulary is cut into parts, a workgroup each, whose
+// sums one more workgroup per row joins to find the token's part; latency and
+// launches bound it.  Measured: 5 nodes in a chain with draft probabilities,
+// 32003 tokens, 19 us a call (kernels 2.3 + 5.2 + 7.3); 32 rows of 16 nodes
+// without, 131072 tokens, 15.6 us (6.7 + 6.8; 17 MB).
 #pragma once
 #include "gdn_common.h"
 
