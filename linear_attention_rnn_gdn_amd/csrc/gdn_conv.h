@@ -12,7 +12,8 @@
 // Measured with W = 4 in bf16, 8192 channels: 4096 tokens forward 29 us (134 MB,
 // 4.6 TB/s; a large copy reaches 5.0 to 5.2 TB/s here), gradients 50 us and 5 for
 // the pieces' sums (202 MB, 3.6 TB/s; the vector ALU is busy 67% of the time),
-// one token of 256 rows 9.6 us (34 MB).
+// one token of 256 rows 9.8 us (34 MB), of 512
+// rows 13.8 us (67 MB, 4.9 TB/s).
 #pragma once
 #include <type_traits>
 
@@ -200,31 +201,28 @@ __global__ __launch_bounds__(256, 4) void conv_fwd_kernel(ConvArgs a) {
 }
 
 // One token of every row: the row's window in the pool [n_slots, W - 1, C]
-// moves on by one token.
-template <int W, int VEC, typename T>
+// moves on by one token.  A thread takes its channels of ROWS rows, which share
+// the reads of the weights (all of a thread's own, and so a line each).
+template <int W, int VEC, int ROWS, typename T>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
   using P = typename Pack<T, VEC>::type;
   const int tid = threadIdx.x, tiles = (a.C / VEC + 255) / 256;
-  const int b = blockIdx.x / tiles, c = (blockIdx.x % tiles * 256 + tid) * VEC;
-  int slot = a.slots ? a.slots[b] : b;
-  if (slot < 0 || slot >= a.n_slots) slot = -1;
-  bool seen = false;   // an earlier row has the slot
-  if (a.slots && slot >= 0)
-    for (int i = tid; i < b; i += 256) seen |= a.slots[i] == slot;
-  if (__syncthreads_or(seen)) slot = -1;
-  if (c >= a.C) return;
-  P *y = reinterpret_cast<P *>(static_cast<T *>(a.y) + (size_t)b * a.C + c);
-  if (slot < 0) {   // no window: a zero output
-    *y = P{};
-    return;
-  }
-  T *st = static_cast<T *>(a.state) + (size_t)slot * (W - 1) * a.C + c;
-  P in[W];
+  const int b0 = blockIdx.x / tiles * ROWS, to = (blockIdx.x % tiles * 256 + tid) * VEC, c = min(to, a.C - VEC);
+  // Everything is asked for before the other rows' slots are looked at (a row
+  // without a slot reads some window, and leaves it).
+  int slot[ROWS];
+  P in[ROWS][W];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) in[k] = *reinterpret_cast<const P *>(st + (size_t)k * a.C);
-  in[W - 1] = *reinterpret_cast<const P *>(static_cast<const T *>(a.x) + b * a.ld + c);
-  float o[VEC], w[W][VEC];
-  // (a row's whole work is a few loads: its own weights in 16 bytes each, at once with the rest, beat a barrier)
+  for (int r = 0; r < ROWS; ++r) {
+    const int b = min(b0 + r, a.B - 1);
+    slot[r] = a.slots ? a.slots[b] : b;
+    if (slot[r] < 0 || slot[r] >= a.n_slots) slot[r] = -1;
+    const T *st = static_cast<const T *>(a.state) + (size_t)max(slot[r], 0) * (W - 1) * a.C + c;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) in[r][k] = *reinterpret_cast<const P *>(st + (size_t)k * a.C);
+    in[r][W - 1] = *reinterpret_cast<const P *>(static_cast<const T *>(a.x) + b * a.ld + c);
+  }
+  float w[W][VEC], bias[VEC];
   const float *wp = a.weight + (size_t)c * W;
   if constexpr (VEC == 1) {
 #pragma unroll
@@ -240,20 +238,41 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
     }
   }
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) o[v] = a.bias ? a.bias[c + v] : 0.f;
+  for (int v = 0; v < VEC; ++v) bias[v] = a.bias ? a.bias[c + v] : 0.f;
 #pragma unroll
-  for (int k = 0; k < W; ++k) {
-    float x[VEC];
-    widen<VEC, T>(in[k], x);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = fmaf(w[k][v], x[v], o[v]);
+  for (int r = 0; r < ROWS; ++r) {
+    bool seen = false;   // an earlier row has the slot
+    if (a.slots && slot[r] >= 0)
+      for (int i = tid; i < b0 + r; i += 256) seen |= a.slots[i] == slot[r];
+    if (__syncthreads_or(seen)) slot[r] = -1;
   }
-  if (a.silu)
+  if (to >= a.C) return;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = silu<true>(o[v]);
+  for (int r = 0; r < ROWS; ++r) {
+    if (b0 + r >= a.B) return;
+    P *y = reinterpret_cast<P *>(static_cast<T *>(a.y) + (size_t)(b0 + r) * a.C + c);
+    if (slot[r] < 0) {   // no window: a zero output
+      *y = P{};
+      continue;
+    }
+    float o[VEC];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) *reinterpret_cast<P *>(st + (size_t)k * a.C) = in[k + 1];
-  *y = narrow<VEC, T>(o);
+    for (int v = 0; v < VEC; ++v) o[v] = bias[v];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      float x[VEC];
+      widen<VEC, T>(in[r][k], x);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) o[v] = fmaf(w[k][v], x[v], o[v]);
+    }
+    if (a.silu)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) o[v] = silu<true>(o[v]);
+    T *st = static_cast<T *>(a.state) + (size_t)slot[r] * (W - 1) * a.C + c;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) *reinterpret_cast<P *>(st + (size_t)k * a.C) = in[r][k + 1];
+    *y = narrow<VEC, T>(o);
+  }
 }
 
 // The gradients.  d[t] = dy[t] act'(pre[t]) from the window, as the forward;

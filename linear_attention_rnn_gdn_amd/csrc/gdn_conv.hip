@@ -25,6 +25,13 @@ constexpr int kFwdRun = 16;
 // channels, 19.7 and 22 at 300 of 512.  (Halving below 1024 took 59 us instead
 // of 53 at the first of these, 19 instead of 19.8 at the last two.)
 constexpr int kBwdRun = 64, kBwdShort = 16, kFewPieces = 512;
+// Single tokens: two rows per thread in bf16 from so many workgroups of one row
+// on, one below and in fp32.  One, two and four rows took, in us: bf16, 64 rows
+// of 8192 channels (256 workgroups) 4.4, 5.1 and 6.6, 128 of them (512) 6.2, 6.1
+// and 7.5, 192 (768) 8.1 and 8.5, 256 (1024) 10.1, 9.8 and 10.7, 512 (2048)
+// 16.4, 13.8 and 14.9; 2048 rows of 4099 channels (single elements) 47 and 40;
+// fp32, 256 rows of 4096 channels 7.5, 8.4 and 9.6, 512 rows of 8192 21.0 and 20.6.
+constexpr int kManySteps = 1024;
 
 int elem(const gdn_conv_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 
@@ -154,12 +161,18 @@ gdn_status gdn_conv_step(const gdn_conv_shape *s, const void *x, const float *we
   return with_pack(*s, wide(*s, {x, state, y, weight}), [&](auto vec, auto t) -> gdn_status {
     constexpr int VEC = decltype(vec)::value;
     using T = decltype(t);
-    const int64_t blocks = (int64_t)s->B * ((s->C / VEC + 255) / 256);
-    if (blocks > kMaxBlocks) return GDN_ERR_SHAPE;
+    const int64_t tiles = (s->C / VEC + 255) / 256;
+    if (s->B * tiles > kMaxBlocks) return GDN_ERR_SHAPE;
     return with_width(s->W, [&](auto w) -> gdn_status {
-      hipLaunchKernelGGL((conv_step_kernel<decltype(w)::value, VEC, T>), dim3((unsigned)blocks), dim3(256), 0,
-                         reinterpret_cast<hipStream_t>(hip_stream), a);
-      return check_launch();
+      auto run = [&](auto rows) -> gdn_status {
+        constexpr int ROWS = decltype(rows)::value;
+        hipLaunchKernelGGL((conv_step_kernel<decltype(w)::value, VEC, ROWS, T>), dim3((unsigned)((s->B + ROWS - 1) / ROWS * tiles)),
+                           dim3(256), 0, reinterpret_cast<hipStream_t>(hip_stream), a);
+        return check_launch();
+      };
+      if constexpr (sizeof(T) == 2)
+        if (s->B * tiles >= kManySteps) return run(std::integral_constant<int, 2>{});
+      return run(std::integral_constant<int, 1>{});
     });
   });
 }

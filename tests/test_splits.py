@@ -121,6 +121,33 @@ def test_convolution_gradients_by_runs_of_every_length(gdn, B, T, C, W, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("B,C", [(1025, 16), (1023, 24), (517, 257), (300, 2056)])
+def test_convolution_steps_of_many_rows(gdn, B, C, W, dtype):
+    # from 1024 workgroups on a thread may take two rows: odd numbers of them, and neighbours that share a slot
+    gen = torch.Generator().manual_seed(B)
+    n = B + 5
+    pool = torch.randn(n, W - 1, C, generator=gen).to(DT[dtype])
+    slots = torch.randperm(n, generator=gen)[:B].to(torch.int32)
+    slots[1], slots[7], slots[10], slots[B - 1] = slots[0], -1, n, slots[B - 2]
+    x = conv._draw([1] * B, C, W, dtype, B, True, False)
+    x["h0"] = torch.stack([pool[s] if 0 <= s < n else torch.zeros(W - 1, C, dtype=pool.dtype) for s in slots.tolist()])
+    ref, err = conv._reference(x, [1] * B, False, True)
+    want, used = conv._np(pool), set()
+    for b, s in enumerate(slots.tolist()):
+        if 0 <= s < n and s not in used:
+            used.add(s)
+            want[s] = ref["h_T"][b]
+        else:
+            ref["y"][b] = err["y"][b] = 0
+    state = pool.cuda()
+    y = gdn.conv_step(x["x"][:, 0].cuda(), x["weight"].cuda(), state, x["bias"].cuda(), slots.cuda())
+    conv._close("y", y, ref["y"][:, 0], err["y"][:, 0])
+    assert np.array_equal(conv._np(state), want)
+
+
+@pytest.mark.gpu
 def test_no_tokens(gdn):
     x = ssm._cuda(ssm._draw([0, 0], 10, 8, 2, "bf16", 1))
     y, hT = gdn.ssm_fwd(**ssm._args(x), h0=x["h0"])
