@@ -12,8 +12,7 @@
 // Measured with W = 4 in bf16, 8192 channels: 4096 tokens forward 29 us (134 MB,
 // 4.6 TB/s; a large copy reaches 5.0 to 5.2 TB/s here), gradients 50 us and 5 for
 // the pieces' sums (202 MB, 3.6 TB/s; the vector ALU is busy 67% of the time),
-// one token of 256 rows 9.8 us (34 MB), of 512
-// rows 13.8 us (67 MB, 4.9 TB/s).
+// one token of 256 rows 9.8 us (34 MB), of 512 rows 13.8 us (67 MB, 4.9 TB/s).
 #pragma once
 #include <type_traits>
 

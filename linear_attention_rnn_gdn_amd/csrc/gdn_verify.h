@@ -23,11 +23,12 @@
 // in order finds the path.  All comparisons and sums are in fp64 of the fp32
 // inputs: they decide tokens.
 //
-// Rows are few, so the vocabulary is cut into parts, a workgroup each, whose
-// sums one more workgroup per row joins to find the token's part; latency and
-// launches bound it.  Measured: 5 nodes in a chain with draft probabilities,
-// 32003 tokens, 19 us a call (kernels 2.3 + 5.2 + 7.3); 32 rows of 16 nodes
-// without, 131072 tokens, 15.6 us (6.7 + 6.8; 17 MB).
+// Rows are few, so a large vocabulary is cut into parts, a workgroup each,
+// whose sums one more workgroup per row joins to find the token's part; of a
+// small one a workgroup per row does it all, in one launch.  Latency and
+// launches bound both.  Measured: 5 nodes in a chain with draft probabilities,
+// 32003 tokens, 12.5 us a call (kernel 11.5 to 13; in three launches 19); 32
+// rows of 16 nodes without, 131072 tokens, 15.0 us a call (kernels 6.7 + 6.8; 17 MB).
 #pragma once
 #include "gdn_common.h"
 
@@ -337,6 +338,96 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a) {
   if (tid) return;
   hit = min(min(hits[0], hits[1]), min(hits[2], hits[3]));
   a.token[b] = hit < 1 << 30 ? hit : max(max(some[0], some[1]), max(some[2], some[3]));
+}
+
+// All of a row by one workgroup, for small vocabularies: the walk, the sums of
+// chunks of 1024 tokens (a wave each; without draft probabilities two at once),
+// and the draw by the first wave.
+constexpr int VERIFY_CHUNK = 1024, VERIFY_CHUNKS = 32;
+template <bool DRAFT>
+__global__ __launch_bounds__(1024) void verify_row_kernel(VerifyArgs a) {
+  constexpr int PER = VERIFY_CHUNK / 64, PAIR = DRAFT ? 1 : 2;
+  __shared__ double red[2][16], sums[VERIFY_CHUNKS];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const double u = (double)a.uniform[(size_t)b * (a.n + 1) + a.n];
+  int mine;
+  const VerifyPlan plan = verify_walk<1024, DRAFT>(a, b, tid, red, mine);
+  if (wave == 0) {
+    if (lane < a.n) a.path[(size_t)b * a.n + lane] = mine;
+    if (lane == 0) a.last[b] = plan.at;
+  }
+  const int chunks = (a.V + VERIFY_CHUNK - 1) / VERIFY_CHUNK;
+  double taken = plan.taken, own, upto, whole;
+  for (bool again = false;; again = true) {
+    for (int k = wave; k < chunks; k += 16 * PAIR) {
+      float p[PAIR][PER], q[PAIR][PER];
+      Residual r[PAIR];
+      int hi[PAIR];
+#pragma unroll
+      for (int m = 0; m < PAIR; ++m) {
+        const int lo = (k + 16 * m) * VERIFY_CHUNK;
+        hi[m] = min(a.V, lo + VERIFY_CHUNK);
+        r[m] = residual_of(a, plan, taken, b, lo, hi[m], lane);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int at = min(lo + lane + i * 64, a.V - 1);   // (a chunk behind the last: read again, and not counted)
+          p[m][i] = r[m].p[at];
+          q[m][i] = DRAFT && r[m].q ? r[m].q[at] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < PAIR; ++m) {
+        double s = 0.;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int v = (k + 16 * m) * VERIFY_CHUNK + lane + i * 64;
+          double w = v < hi[m] ? positive(DRAFT ? fma(-taken, (double)q[m][i], (double)p[m][i]) : (double)p[m][i]) : 0.;
+          if constexpr (!DRAFT)
+            for (unsigned long long left = r[m].refused; left; left &= left - 1)   // (uniform, and mostly none)
+              w = v == r[m].tokens[__ffsll((long long)left) - 1] ? 0. : w;
+          s += w;
+        }
+        s = wave_sum(s);
+        if (lane == 0 && k + 16 * m < chunks) sums[k + 16 * m] = s;
+      }
+    }
+    __syncthreads();
+    own = lane < chunks ? sums[lane] : 0.;
+    upto = wave_scan(own, lane);
+    whole = __shfl(upto, 63);
+    if (whole > 0. || again || plan.before < 0.) break;   // uniform
+    taken = plan.before;   // a residual without mass is not taken
+    __syncthreads();
+  }
+  if (wave) return;
+  const double mark = u * whole;
+  const unsigned long long pass = __ballot(own > 0. && upto > mark);
+  if (!pass) {   // no mass (or no number)
+    if (lane == 0) a.token[b] = -1;
+    return;
+  }
+  const int who = __ffsll((long long)pass) - 1;
+  const int lo = who * VERIFY_CHUNK, hi = min(a.V, lo + VERIFY_CHUNK);
+  double w[PER], sum = 0., run = __shfl(upto - own, who);
+  weights<PER>(residual_of(a, plan, taken, b, lo, hi, lane), lo + lane * PER, 1, hi, w);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += w[i];
+  run += wave_scan(sum, lane) - sum;
+  int hit = 1 << 30, any = -1;   // the lane's first token at which the sum passes, and its last with a weight
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    run += w[i];
+    if (w[i] > 0.) {
+      any = lo + lane * PER + i;
+      if (run > mark) hit = min(hit, any);
+    }
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    hit = min(hit, __shfl_xor(hit, m));
+    any = max(any, __shfl_xor(any, m));
+  }
+  if (lane == 0) a.token[b] = hit < 1 << 30 ? hit : any;
 }
 
 }  // namespace gdn

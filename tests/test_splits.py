@@ -260,6 +260,33 @@ def test_large_vocabularies(gdn, draft):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("B,V", [(2, 32768), (2, 32769), (32, 700), (33, 700)])
+def test_verification_in_one_launch_and_in_several(gdn, B, V, draft):
+    # on both sides of where the forms change: siblings refused in a row, absent nodes and rows, rows without mass
+    x = verify._draw(B, 12, V, V + B, draft, near=0.0)
+    verify._same(gdn, x)
+    x["parents"][:] = -1
+    x["tokens"][:, 1::2] = x["tokens"][:, ::2]
+    x["uniform"][:, :12] = 1 - 2.0 ** -24
+    verify._same(gdn, x)
+    x["parents"][0], x["parents"][1, 3:] = -2, 2
+    x["tokens"][1, 0], x["tokens"][1, 5] = -1, V
+    x["target"][0] = 0.0
+    x["target"][1, :, ::3] *= -1
+    x["target"][1, 0, 5:9] = float("nan")
+    for u in (0.0, 0.5, 1 - 2.0 ** -24):
+        x["uniform"][:, 12] = u
+        verify._same(gdn, x)
+    if draft:   # the last refusal leaves no mass
+        x["target"][:, 0] = x["draft"][:, 0]
+        x["parents"][:], x["parents"][:, 0] = -2, -1
+        x["target"][:, 0, 17], x["tokens"][:, 0] = 0, 17
+        want = verify._same(gdn, x)
+        assert (want[0] == -1).all() and (want[1] >= 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("draft", [True, False])
 def test_probabilities_past_32_bits(gdn, draft):
     B, n, V = 9, 64, 3_800_001
     gen = torch.Generator(device="cuda").manual_seed(9)
