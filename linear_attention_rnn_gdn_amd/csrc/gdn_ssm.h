@@ -15,8 +15,8 @@
 // a second carries the states from segment to segment (the decay of a whole
 // segment is e^{A sum d}), and the walks start from those.
 // Measured at 4096 tokens of 4096 channels with 16 states in bf16 (vector ALU
-// busy; its instructions per token and wave): forward 138 us = folds 59 (89%;
-// 89) + scan 12 + walks 80 (88%; 123), of which 5 N are the recurrence's own;
+// busy; its instructions per token and wave): forward 135 us = folds 58 (91%;
+// 89) + scan 12 + walks 78 (91%; 121), of which 5 N are the recurrence's own;
 // gradients 401 us = folds 104 (86%; 153) + scan 19 + walks 300 (81%; 449) +
 // sums 11.  One token of 256 rows with 4096 channels: 28 us, 143 MB, 5.0 TB/s.
 #pragma once
@@ -121,12 +121,14 @@ __device__ __forceinline__ void store_states(float *p, const float (&h)[N]) {
 
 __device__ __forceinline__ float step_size(const SsmArgs &a, float v) { return a.softplus ? softplus(v, exp_neg_abs(v)) : v; }
 
-// Tokens asked for at once, and worked on without a branch between them (8 in the walk took 140 us instead of
-// 144; the fold for the gradients notes states between batches, at every 4th or 8th token).
-constexpr int SSM_BATCH = 4;
+// Tokens asked for at once, and worked on without a branch between them, by the
+// walk (4 took 143 and 178 us instead of 140 and 176 at 4096 x 4096 and at 12
+// packed sequences, 16 states; 247 instead of 239 with 32) and by the fold of
+// the gradients, which notes states between batches, at every 4th or 8th token.
+constexpr int WALK_BATCH = 8, FOLD_BATCH = 4;
 
 // One wave: 64 channels of one segment.  FOLD: only the segment's end state
-// and sum of d.  The elements of the next SSM_BATCH tokens are on their way
+// and sum of d.  The elements of the next WALK_BATCH tokens are on their way
 // while these are worked on, and so are B and C of the next token.
 // A batch in which the segment or a sequence ends is walked token by token.
 //
@@ -194,13 +196,13 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
     for (int n = 0; n < N; ++n) h[n] = a.in[se + n * 64];
   float sum = 0.f;
   struct Batch {
-    TI x[SSM_BATCH], dt[SSM_BATCH], z[SSM_BATCH];
+    TI x[WALK_BATCH], dt[WALK_BATCH], z[WALK_BATCH];
   };
   // asks for the elements of the tokens from the pointers' on (past the segment's last: of that one again)
   auto ask = [&](int left, Batch &p) {
     const unsigned off = fresh_offset(ci);
 #pragma unroll
-    for (int i = 0; i < SSM_BATCH; ++i) {
+    for (int i = 0; i < WALK_BATCH; ++i) {
       const int64_t at = min(i, left - 1);
       p.x[i] = raw(x + at * a.ld_x, off);
       p.dt[i] = raw(dt + at * a.ld_dt, off);
@@ -217,15 +219,15 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
   if (AHEAD && t0 < t1) ask_rows(B, C);
   Batch now, next;
   if (t0 < t1) ask(t1 - t0, now);
-  for (int t = t0; t < t1; t += SSM_BATCH) {
-    const bool whole = t + SSM_BATCH <= t1 && (q.end <= t || q.end >= t + SSM_BATCH);
-    x += SSM_BATCH * a.ld_x;
-    dt += SSM_BATCH * a.ld_dt;
-    z += SSM_BATCH * ld_z;
-    if (t + SSM_BATCH < t1) ask(t1 - t - SSM_BATCH, next);
-    float xs[SSM_BATCH], d[SSM_BATCH];
+  for (int t = t0; t < t1; t += WALK_BATCH) {
+    const bool whole = t + WALK_BATCH <= t1 && (q.end <= t || q.end >= t + WALK_BATCH);
+    x += WALK_BATCH * a.ld_x;
+    dt += WALK_BATCH * a.ld_dt;
+    z += WALK_BATCH * ld_z;
+    if (t + WALK_BATCH < t1) ask(t1 - t - WALK_BATCH, next);
+    float xs[WALK_BATCH], d[WALK_BATCH];
 #pragma unroll
-    for (int i = 0; i < SSM_BATCH; ++i) {
+    for (int i = 0; i < WALK_BATCH; ++i) {
       xs[i] = to_f32(now.x[i]);
       d[i] = step_size(a, to_f32(now.dt[i]) + bias);
     }
@@ -278,11 +280,11 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
     };
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < SSM_BATCH; ++i) token(i);
-      sequence_end(SSM_BATCH - 1);
+      for (int i = 0; i < WALK_BATCH; ++i) token(i);
+      sequence_end(WALK_BATCH - 1);
     } else {
 #pragma unroll
-      for (int i = 0; i < SSM_BATCH; ++i) {
+      for (int i = 0; i < WALK_BATCH; ++i) {
         if (t + i >= t1) break;
         token(i);
         sequence_end(i);
@@ -455,12 +457,12 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
   }
   float sum = 0.f;
   struct Batch {
-    TI x[SSM_BATCH], dt[SSM_BATCH], z[SSM_BATCH], dy[SSM_BATCH];
+    TI x[FOLD_BATCH], dt[FOLD_BATCH], z[FOLD_BATCH], dy[FOLD_BATCH];
   };
   auto ask = [&](int k, Batch &p) {
     const unsigned off = fresh_offset(ci);
 #pragma unroll
-    for (int i = 0; i < SSM_BATCH; ++i) {
+    for (int i = 0; i < FOLD_BATCH; ++i) {
       const int64_t at = min(k + i, len - 1);
       p.x[i] = raw(x + at * a.ld_x, off);
       p.dt[i] = raw(dt + at * a.ld_dt, off);
@@ -475,17 +477,17 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
     B.load(Bm);
     C.load(Cm);
   }
-  for (int k = 0; k < len; k += SSM_BATCH) {
-    if (k + SSM_BATCH < len) ask(k + SSM_BATCH, next);
+  for (int k = 0; k < len; k += FOLD_BATCH) {
+    if (k + FOLD_BATCH < len) ask(k + FOLD_BATCH, next);
     if (k && k % SsmBwd<N>::S == 0) {
       const size_t m = ((size_t)unit * a.marks + k / SsmBwd<N>::S - 1) * a.tiles + tile;
       a.mark_sum[m * 64 + lane] = sum;
 #pragma unroll
       for (int n = 0; n < N; ++n) a.mark[(m * N + n) * 64 + lane] = h[n];
     }
-    float d[SSM_BATCH], u[SSM_BATCH], g[SSM_BATCH];
+    float d[FOLD_BATCH], u[FOLD_BATCH], g[FOLD_BATCH];
 #pragma unroll
-    for (int i = 0; i < SSM_BATCH; ++i) {   // (a token past the last: no step, no cotangent)
+    for (int i = 0; i < FOLD_BATCH; ++i) {   // (a token past the last: no step, no cotangent)
       const bool here = k + i < len;
       d[i] = here ? step_size(a, to_f32(now.dt[i]) + bias) : 0.f;
       u[i] = here ? d[i] * to_f32(now.x[i]) : 0.f;
@@ -494,7 +496,7 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
       sum += d[i];
     }
 #pragma unroll
-    for (int i = 0; i < SSM_BATCH; ++i) {
+    for (int i = 0; i < FOLD_BATCH; ++i) {
       const int64_t at = min(k + i + (AHEAD ? 1 : 0), len - 1);
       if constexpr (AHEAD) {
         B.wait();

@@ -17,7 +17,8 @@ constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 thr
 // Segments of a forward pass: as many as give 4096 walks, four per SIMD.  At
 // 4096 tokens of 4096 channels with 16 states, and at 12 packed sequences (9925
 // tokens) of 2000 channels, 1024 walks took 364 and 425 us, 2048 190 and 235, 4096 144 and
-// 179, 8192 154 and 188 (a segment more costs its state's two passes).
+// 179, 8192 154 and 188 (a segment more costs its state's two passes; measured
+// with batches of 4 tokens in the walk, which has 8 now).
 constexpr int kWaves = 4096;
 // ... of 16 tokens or more: 8, 16, 32 and 64 took 26, 27, 36 and 60 us at 512
 // tokens of 512 channels, 48, 38, 40 and 62 at 2048 tokens of them, and 106 and
@@ -99,7 +100,7 @@ Layout layout_ssm(const gdn_ssm_shape &s, const SsmArgs &a, bool grads) {
   } else {
     const int64_t walks = (int64_t)a.rows * a.tiles, want = std::max<int64_t>(1, kWaves / walks);
     const int64_t len = (s.T + want - 1) / want;
-    l.len = (int)std::max<int64_t>(kShortest, (len + SSM_BATCH - 1) / SSM_BATCH * SSM_BATCH);
+    l.len = (int)std::max<int64_t>(kShortest, (len + WALK_BATCH - 1) / WALK_BATCH * WALK_BATCH);
     l.J = (int)(((int64_t)s.T + l.len - 1) / l.len);
   }
   size_t off = 0;

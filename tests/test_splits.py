@@ -58,7 +58,7 @@ def test_gradients_by_segments_of_every_length(gdn, B, T, C, G, N, dtype):
 @pytest.mark.parametrize("B,T,C,G", [
     (8, 300, 64, 64),     # 512 walks: 8 segments of 40
     (17, 30, 256, 256),   # 4352: one segment each
-    (16, 130, 70, 70),    # 1120: segments of 44
+    (16, 130, 70, 70),    # 1120: segments of 48
     (1, 1500, 3, 1),      # 94 segments of 16
 ])
 def test_forward_by_segments_of_every_length(gdn, B, T, C, G, N):
