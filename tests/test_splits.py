@@ -287,6 +287,59 @@ def test_verification_in_one_launch_and_in_several(gdn, B, V, draft):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("draft", [True, False])
+def test_verification_in_several_launches_on_streams_and_in_a_graph(gdn, draft):
+    x = {k: None if t is None else t.cuda() for k, t in verify._draw(5, 12, 40001, 14, draft).items()}
+    call = lambda **kw: gdn.tree_verify(x["tokens"], x["parents"], x["target"], x["uniform"], draft=x["draft"], **kw)
+    ref = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, here = call(stream=side), call()
+    side.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(ref, got, here))
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(ref, call(workspace=ws)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, held))
+        for t in held:
+            t.fill_(-9)
+        assert all(torch.equal(a, b) for a, b in zip(ref, call()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_steps_in_a_graph(gdn, dtype):
+    # a token's convolution and scan captured together: every replay moves the pools on by one token, as eager calls do
+    B, C, N = 3, 72, 16
+    x = ssm._cuda(ssm._draw([1] * B, C, N, 2, dtype, 15, True, True))
+    one = {k: v[:, 0].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in ssm._args(x).items()}
+    gen = torch.Generator().manual_seed(16)
+    u, w = torch.randn(B, C, generator=gen).to(DT[dtype]).cuda(), torch.randn(C, 4, generator=gen).cuda()
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    states = torch.randn(6, C, N, generator=gen).cuda(), torch.randn(6, 3, C, generator=gen).to(DT[dtype]).cuda()
+
+    def token(state, window):
+        v = gdn.conv_step(u, w, window, slots=slots)
+        return gdn.ssm_step(**{**one, "x": v}, state=state, slots=slots)
+
+    eager, held = [t.clone() for t in states], [t.clone() for t in states]
+    token(*[t.clone() for t in states])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = token(*held)
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        want = token(*eager)
+        assert torch.equal(y, want) and all(torch.equal(a, b) for a, b in zip(held, eager))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("draft", [True, False])
 def test_probabilities_past_32_bits(gdn, draft):
     B, n, V = 9, 64, 3_800_001
     gen = torch.Generator(device="cuda").manual_seed(9)
