@@ -634,8 +634,8 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, con
  *   last     [B] the last node accepted, -1: none; token [B] the next token;
  *   path     [B, n] the nodes accepted, in order, then -1 (all int32, written)
  * Rows of target and draft that the walk does not reach are not read, but for
- * single values.  Weights that are negative or no numbers count as zero.  Sums
- * and comparisons are fp64.  B <= 2^20, B * ceil(V / 4096) <= 2^23. */
+ * single values.  Probabilities of either that are negative or no numbers count
+ * as zero.  Sums and comparisons are fp64.  B <= 2^20, B * ceil(V / 4096) <= 2^23. */
 typedef struct {
   int32_t B, n, V;
 } gdn_verify_shape;

@@ -54,15 +54,19 @@ struct VerifyArgs {
 };
 
 __device__ __forceinline__ double positive(double x) { return x > 0. ? x : 0.; }   // (no number: nothing)
+// max(p - t q, 0), but p at most: a draft value below zero, or one that is no
+// number (fmin takes the other of the two), counts as zero, as in the tests of
+// the children.  One instruction more, and behind the loads.
+__device__ __forceinline__ double residual(float p, float q, double t) {
+  return positive(fmin(fma(-t, (double)q, (double)p), (double)p));
+}
 
 // sum of max(p - t q, 0) over tokens lo .. hi - 1 by THREADS threads, this thread's share
 template <int THREADS>
 __device__ __forceinline__ double residual_share(const float *p, const float *q, double t, int lo, int hi, int tid) {
   double s = 0.;
   for (int v = lo + tid; v < hi; v += THREADS) {
-    double x = (double)p[v];
-    if (q) x = fma(-t, (double)q[v], x);
-    s += positive(x);
+    s += q ? residual(p[v], q[v], t) : positive((double)p[v]);
   }
   return s;
 }
@@ -187,7 +191,7 @@ __device__ __forceinline__ void weights(const Residual &r, int v, int step, int 
     q[i] = r.q ? r.q[at] : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < COUNT; ++i) w[i] = v + i * step < hi ? positive(fma(-r.t, (double)q[i], (double)p[i])) : 0.;
+  for (int i = 0; i < COUNT; ++i) w[i] = v + i * step < hi ? residual(p[i], q[i], r.t) : 0.;
   for (unsigned long long m = r.refused; m; m &= m - 1) {   // (uniform, and mostly none)
     const int x = r.tokens[__ffsll((long long)m) - 1];
 #pragma unroll
@@ -381,7 +385,7 @@ __global__ __launch_bounds__(1024) void verify_row_kernel(VerifyArgs a) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int v = (k + 16 * m) * VERIFY_CHUNK + lane + i * 64;
-          double w = v < hi[m] ? positive(DRAFT ? fma(-taken, (double)q[m][i], (double)p[m][i]) : (double)p[m][i]) : 0.;
+          double w = v < hi[m] ? (DRAFT ? residual(p[m][i], q[m][i], taken) : positive((double)p[m][i])) : 0.;
           if constexpr (!DRAFT)
             for (unsigned long long left = r[m].refused; left; left &= left - 1)   // (uniform, and mostly none)
               w = v == r[m].tokens[__ffsll((long long)left) - 1] ? 0. : w;

@@ -230,3 +230,32 @@ def test_refusals(gdn):
                                                    torch.ones(1, 66, 3, device="cuda"), torch.zeros(1, 66, device="cuda")))):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("V", [60, 1001, 9000, 32768, 32769, 40003])
+def test_draft_values_below_zero_or_no_numbers_count_as_zero(gdn, V, tree):
+    # the reference takes the draft with zeros in their place; most of the target's mass lies on tokens whose draft value is no
+    # number, or every token without a probability has one below zero, so that a residual which took these as they are would
+    # lose the one and draw the other
+    x = _draw(4, 10, V, V + tree, True, tree, near=0.0)
+    if tree:
+        x["parents"][:3] = -1
+    bad = torch.arange(V) % 5 == 2
+    x["target"][0, :, bad] *= 50
+    x["draft"][0, :, bad] = float("nan")
+    x["target"][1, :, bad] = 0
+    x["draft"][1, :, bad] = -0.25
+    x["draft"][2] = float("nan")
+    x["draft"][3, :, bad] *= -1
+    clean = dict(x, draft=torch.nan_to_num(x["draft"], nan=0.0).clamp(min=0))
+    for refuse in (False, True):
+        if refuse:
+            x["uniform"][:, :10] = 1 - 2.0 ** -24
+        for u in (0.0, 0.3, 0.7, 1 - 2.0 ** -24):
+            x["uniform"][:, 10] = u
+            want = _reference(clean)
+            got = gdn.tree_verify(*(x[k].cuda() for k in ("tokens", "parents", "target", "uniform")), draft=x["draft"].cuda())
+            for name, a, b in zip(("last", "token", "path"), got, want):
+                assert torch.equal(a.cpu(), b), (name, refuse, u, a.cpu(), b)
