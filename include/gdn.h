@@ -502,9 +502,8 @@ gdn_status gdn_linear_chunk_bwd(const gdn_linear_shape *shape, const void *q, co
  *            gradients are fp32
  * Pointers have to be aligned to an element only; rows that are whole 16-byte
  * pieces (C and ld multiples of 16 bytes, pointers 16-byte aligned) are faster.
- * Sums are fp32, rounded once.  B <= 2^24, C <= 2^20, T <= 2^30, ld <= 2^20 but in
- * gdn_conv_step (any ld >= C), and a launch has to stay below 2^32 threads
- * (GDN_ERR_SHAPE). */
+ * Sums are fp32, rounded once.  B <= 2^24, C, ld <= 2^20, T <= 2^30, and a launch has to
+ * stay below 2^32 threads (GDN_ERR_SHAPE). */
 typedef struct {
   int32_t B, T, C, W, ld, n_slots, silu, dtype;
 } gdn_conv_shape;

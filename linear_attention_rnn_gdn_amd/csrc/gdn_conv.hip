@@ -14,7 +14,7 @@ using namespace gdn;
 namespace {
 
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of 256 threads: a launch holds fewer than 2^32
-constexpr int kMaxRow = 1 << 20;                  // channels, and elements from a token to the next (see lay_out; a step has no such limit)
+constexpr int kMaxRow = 1 << 20;                  // elements from a token to the next (see lay_out)
 // Tokens per thread, rounded down to whole windows.  Forward: at 4096 tokens of
 // 8192 channels in bf16 8 took 33 us (each thread reads its W - 1 tokens of
 // window too), 16 30 and 32 32.4 (too few waves).
@@ -35,11 +35,11 @@ constexpr int kManySteps = 1024;
 
 int elem(const gdn_conv_shape &s) { return s.dtype == GDN_BF16 ? 2 : 4; }
 
-gdn_status validate_conv(const gdn_conv_shape *s, bool step = false) {
+gdn_status validate_conv(const gdn_conv_shape *s) {
   if (!s) return GDN_ERR_NULL;
   if (s->dtype != GDN_F32 && s->dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (s->B < 1 || s->B > 1 << 24 || s->T < 0 || s->T > 1 << 30 || s->C < 1 || s->C > kMaxRow || s->W < 2 || s->W > 4) return GDN_ERR_SHAPE;
-  if ((s->ld && (s->ld < s->C || (!step && s->ld > kMaxRow))) || (s->silu & ~1)) return GDN_ERR_SHAPE;
+  if ((s->ld && (s->ld < s->C || s->ld > kMaxRow)) || (s->silu & ~1)) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 
@@ -152,7 +152,7 @@ gdn_status gdn_conv_fwd_varlen(const gdn_conv_shape *s, const int32_t *cu_seqlen
 
 gdn_status gdn_conv_step(const gdn_conv_shape *s, const void *x, const float *weight, const float *bias, const int32_t *slots,
                          void *state, void *y, void *hip_stream) {
-  GDN_TRY(validate_conv(s, true));
+  GDN_TRY(validate_conv(s));
   if (s->T != 1 || s->n_slots < 1 || (!slots && s->n_slots < s->B)) return GDN_ERR_SHAPE;
   if (!x || !weight || !state || !y) return GDN_ERR_NULL;
   GDN_TRY(aligned(*s, {x, state, y}, {weight, bias, slots}));
