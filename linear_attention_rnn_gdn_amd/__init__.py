@@ -908,6 +908,7 @@ def _conv_plan(grads, *sizes):
     return shape, int(n.value)
 
 
+_CONV_ROW = 1 << 20   # elements from a token of x to the next, at most
 _ACTIVATIONS = {None: 0, "silu": 1}
 
 
@@ -1017,10 +1018,11 @@ def _check_grads(want, out, workspace, inputs, dev):
 
 
 def conv_step(x, weight, state, bias=None, slots=None, activation="silu", out=None, stream=None):
-    """One token of every row (gdn_conv_step), for decoding: x [B,C]; state
-    [n_slots,W-1,C] in x's dtype, a pool of windows moved on in place; slots as
-    in step.  A row without a slot, or with an earlier row's, gets a zero output
-    and writes no window.  Returns y [B,C]."""
+    """One token of every row (gdn_conv_step), for decoding: x [B,C] (rows more
+    than 2^20 elements apart are copied first); state [n_slots,W-1,C] in x's
+    dtype, a pool of windows moved on in place; slots as in step.  A row without
+    a slot, or with an earlier row's, gets a zero output and writes no window.
+    Returns y [B,C]."""
     ld, C, W = _conv_inputs(x, weight, bias, 2)
     silu, dev, dt, B = _activation(activation), x.device, x.dtype, x.shape[0]
     n_slots = _leading(state, "state", 3)[0]
@@ -1030,8 +1032,11 @@ def conv_step(x, weight, state, bias=None, slots=None, activation="silu", out=No
     if out is not None:
         _check_tensors(dev, (out, "y", dt, (B, C)))
         _check_apart(((out, "y"),), ((x, "x"), (weight, "weight"), (bias, "bias"), (state, "state"), (slots, "slots")))
-    shape, _ = _conv_plan(False, B, 1, C, W, ld, n_slots, silu, _dt(dt))
+    far = ld > _CONV_ROW   # (one token of longer prompts, say: the library's limit, so the rows are brought together)
+    shape, _ = _conv_plan(False, B, 1, C, W, 0 if far else ld, n_slots, silu, _dt(dt))
     with _on(dev, stream) as st:
+        if far:
+            x = x.contiguous()
         y = torch.empty((B, C), dtype=dt, device=dev) if out is None else out
         _check(lib().gdn_conv_step(shape, _addr(x), _addr(weight), _addr(bias), _addr(slots), _addr(state), _addr(y), st),
                "gdn_conv_step")

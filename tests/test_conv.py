@@ -319,3 +319,54 @@ def test_refusals(gdn):
             (TypeError, lambda: gdn.conv_step(X[:, 0], w, x["h0"], slots=torch.zeros(2, device="cuda")))):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [8192, 8191])
+def test_steps_of_rows_far_apart(gdn, dtype, C):
+    # one token of a batch of longer prompts: the rows lie more than 2^20 elements apart
+    prompts = torch.randn(3, 130, C, device="cuda").to(DT[dtype])
+    w, state = torch.randn(C, 4, device="cuda"), torch.randn(3, 3, C, device="cuda").to(DT[dtype])
+    assert prompts[:, 77].stride(0) > 1 << 20
+    s2 = state.clone()
+    y = gdn.conv_step(prompts[:, 77], w, state)
+    assert torch.equal(y, gdn.conv_step(prompts[:, 77].contiguous(), w, s2)) and torch.equal(state, s2)
+
+
+@pytest.mark.gpu
+def test_steps_of_rows_as_far_apart_as_they_may_be(gdn):
+    apart, C = (1 << 31) - 1, 24
+    room = torch.empty(apart + C, device="cuda", dtype=torch.bfloat16)
+    x, small = room.as_strided((2, C), (apart, 1)), torch.randn(2, C, device="cuda").bfloat16()
+    x.copy_(small)
+    w, state = torch.randn(C, 3, device="cuda"), torch.randn(2, 2, C, device="cuda").bfloat16()
+    s2 = state.clone()
+    assert torch.equal(gdn.conv_step(x, w, state), gdn.conv_step(small, w, s2)) and torch.equal(state, s2)
+    with pytest.raises(gdn.GdnError):   # (a prompt's tokens may not)
+        gdn.conv_fwd(x.unsqueeze(0), w)
+    with pytest.raises(gdn.GdnError):
+        gdn.conv_bwd(x.unsqueeze(0), w, small.unsqueeze(0))
+
+
+@pytest.mark.gpu
+def test_steps_of_rows_far_apart_on_a_stream_and_in_a_graph(gdn):
+    C = 8192
+    prompts, w, first = torch.randn(3, 130, C, device="cuda").bfloat16(), torch.randn(C, 4, device="cuda"), torch.randn(4, 3, C, device="cuda").bfloat16()
+    slots = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
+    eager, held, aside = first.clone(), first.clone(), first.clone()
+    want = gdn.conv_step(prompts[:, 5].contiguous(), w, eager, slots=slots)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = gdn.conv_step(prompts[:, 5], w, aside, slots=slots, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(aside, eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = gdn.conv_step(prompts[:, 5], w, held, slots=slots)
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(held, eager)
+        prompts[:, 5] = torch.randn(3, C, device="cuda").bfloat16()
+        want = gdn.conv_step(prompts[:, 5].contiguous(), w, eager, slots=slots)
