@@ -869,8 +869,10 @@ def _columns(t, name, dtype, shape, dev, tail):
         after *= n
     if ld is None:
         return 0
-    if not width <= ld < 1 << 31:
+    if ld < width:
         raise ValueError(f"{name}: tokens must not overlap")
+    if ld >= 1 << 31:
+        raise ValueError(f"{name}: tokens must be fewer than 2^31 elements apart")
     return ld
 
 

@@ -370,3 +370,15 @@ def test_steps_of_rows_far_apart_on_a_stream_and_in_a_graph(gdn):
         assert torch.equal(y, want) and torch.equal(held, eager)
         prompts[:, 5] = torch.randn(3, C, device="cuda").bfloat16()
         want = gdn.conv_step(prompts[:, 5].contiguous(), w, eager, slots=slots)
+
+
+@pytest.mark.gpu
+def test_rows_too_far_apart_are_called_that(gdn):
+    C = 16
+    room = torch.empty((1 << 31) + C, device="cuda", dtype=torch.bfloat16)
+    x, w, state = room.as_strided((2, C), (1 << 31, 1)), torch.randn(C, 4, device="cuda"), torch.zeros(2, 3, C, device="cuda", dtype=torch.bfloat16)
+    for call in (lambda: gdn.conv_step(x, w, state), lambda: gdn.conv_fwd(x.unsqueeze(0), w)):
+        with pytest.raises(ValueError, match="x: tokens must be fewer than 2\\^31 elements apart"):
+            call()
+    with pytest.raises(ValueError, match="x: tokens must not overlap"):
+        gdn.conv_step(room.as_strided((2, C), (C - 1, 1)), w, state)
