@@ -492,7 +492,7 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_fold_kernel(SsmArgs a) {
       d[i] = here ? step_size(a, to_f32(now.dt[i]) + bias) : 0.f;
       u[i] = here ? d[i] * to_f32(now.x[i]) : 0.f;
       g[i] = here ? to_f32(now.dy[i]) : 0.f;
-      g[i] *= gated ? silu<std::is_same<TI, __bf16>::value>(to_f32(now.z[i])) : 1.f;
+      g[i] *= gated ? silu<false>(to_f32(now.z[i])) : 1.f;   // (it enters dA and dh0, which are fp32)
       sum += d[i];
     }
 #pragma unroll

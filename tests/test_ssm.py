@@ -474,3 +474,24 @@ def test_refusals(gdn):
         gdn.ssm_bwd(**a, dy=x["dy"], out=dict(g, dx=a["x"]))
     with pytest.raises(ValueError, match="ddt overlaps dx"):
         gdn.ssm_bwd(**a, dy=x["dy"], out=dict(g, ddt=g["dx"]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [8, 16, 32])
+def test_gates_far_below_zero_keep_their_precision_in_the_gradients(gdn, N):
+    # dh0 through segments behind the first, without decay (A = 0): the sum over 17 tokens of C dy silu(z), one channel per z.
+    # silu is good to 8 roundings; a term has 3 products more, a sum of 17 terms at most 17 + 3: 31 roundings of positive terms.
+    # (An exponent z log2(e) that is only rounded is off by half a unit in the place of 64 to 128 times the slope ln 2: up to
+    # 45 roundings of the result, and 20 more by the rounding of log2(e).)
+    gates = (-40 - torch.arange(161) * 0.25).bfloat16().unique()
+    n, T = gates.numel(), 25
+    z = gates.expand(1, T, n).contiguous()
+    dy = torch.ones(1, T, n).bfloat16()
+    dy[:, :8] = 0
+    rows = torch.ones(1, T, 1, N).bfloat16()
+    x = dict(x=torch.ones(1, T, n).bfloat16(), dt=torch.ones(1, T, n).bfloat16(), A=torch.zeros(n, N), B=rows, C=rows, z=z)
+    got = gdn.ssm_bwd(**_cuda(x), dy=dy.cuda())["dh0"].cpu().double()
+    want = 17 * _silu(gates.double()).view(1, n, 1).expand(1, n, N)
+    off = ((got - want) / want).abs().max() / U
+    print(f"  dh0: {float(off):.1f} roundings", flush=True)
+    assert off <= 31
