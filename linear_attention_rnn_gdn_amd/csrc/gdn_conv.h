@@ -347,7 +347,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void conv_bwd_kernel(C
           }
           d[i][v] = t < a.T ? d[i][v] : 0.f;
         }
-        if (own)
+        if (own && t < a.T)   // (none past the last: x there is the last token's again, and zero times that may be no number)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) {
             db[v] += d[i][v];

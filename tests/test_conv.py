@@ -382,3 +382,22 @@ def test_rows_too_far_apart_are_called_that(gdn):
             call()
     with pytest.raises(ValueError, match="x: tokens must not overlap"):
         gdn.conv_step(room.as_strided((2, C), (C - 1, 1)), w, state)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("T,C", [(1, 16), (5, 8), (40, 16), (64, 24), (131, 17)])
+def test_a_bad_last_token_stays_with_its_tap(gdn, T, C, W, dtype):
+    # without an activation a gradient of the weights is a sum of d[t] x[t - (W - 1) + w]: the last token's x is in the last tap's alone
+    x = _cuda(_draw([T, T], C, W, dtype, 17 + T, h0=False))
+    call = lambda v: gdn.conv_bwd(v, x["weight"], x["dy"], x["bias"], dh_T=x["dh_T"], activation=None)
+    clean = call(x["x"])
+    bad = x["x"].clone()
+    bad[0, -1, 3], bad[1, -1, 5], bad[1, -1, C - 1] = float("inf"), float("nan"), -float("inf")
+    got = call(bad)
+    for k in ("dx", "dbias", "dh0"):
+        assert torch.equal(got[k], clean[k]), k
+    touched = torch.zeros_like(got["dweight"], dtype=torch.bool)
+    touched[[3, 5, C - 1], W - 1] = True
+    assert torch.equal(got["dweight"][~touched], clean["dweight"][~touched]) and not got["dweight"][touched].isfinite().any()
