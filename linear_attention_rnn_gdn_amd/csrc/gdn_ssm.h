@@ -739,30 +739,32 @@ __global__ __launch_bounds__(64 * SsmBwd<N>::WAVES, 2) void ssm_bwd_kernel(SsmAr
       }
       __builtin_amdgcn_sched_barrier(0);
       const float u = d * xs[i], g = gs[i];
-      float *to = a.part_bc + ((r0 + min(k + i, len - 1)) * a.tiles + tile) * 2 * N + n0;
       float s = 0.f, du = 0.f, dd = 0.f;
+      if (k + i < len) {   // (nothing of a token past the last: zero times a state behind a bad last token may be no number)
+        float *to = a.part_bc + ((r0 + k + i) * a.tiles + tile) * 2 * N + n0;
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        s = fmaf(C.at(n), hs[i + 1][n], s);
-        r[n] = g * hs[i + 1][n];
-      }
-      reduce_lanes<NS>(r, lane);
-      const float rc = r[0];
-      __builtin_amdgcn_sched_barrier(0);
+        for (int n = 0; n < NS; ++n) {
+          s = fmaf(C.at(n), hs[i + 1][n], s);
+          r[n] = g * hs[i + 1][n];
+        }
+        reduce_lanes<NS>(r, lane);
+        const float rc = r[0];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        dh[n] = fmaf(C.at(n), g, dh[n]);
-        r[n] = u * dh[n];
-        du = fmaf(B.at(n), dh[n], du);
-        dh[n] *= __builtin_amdgcn_exp2f(d * A[n]);
-        const float q = hs[i][n] * dh[n];
-        dd = fmaf(A[n], q, dd);
-        dA[n] = fmaf(d, q, dA[n]);
-      }
-      reduce_lanes<NS>(r, lane);
-      if (k + i < len && reduced_writer<NS>(lane)) {
-        put(to, cr, r[0]);
-        put(to + N, cr, rc);
+        for (int n = 0; n < NS; ++n) {
+          dh[n] = fmaf(C.at(n), g, dh[n]);
+          r[n] = u * dh[n];
+          du = fmaf(B.at(n), dh[n], du);
+          dh[n] *= __builtin_amdgcn_exp2f(d * A[n]);
+          const float q = hs[i][n] * dh[n];
+          dd = fmaf(A[n], q, dd);
+          dA[n] = fmaf(d, q, dA[n]);
+        }
+        reduce_lanes<NS>(r, lane);
+        if (reduced_writer<NS>(lane)) {
+          put(to, cr, r[0]);
+          put(to + N, cr, rc);
+        }
       }
       asm volatile("" : "+v"(s), "+v"(du), "+v"(dd));   // (summed here, not where they are used)
       sum[i][0] = s;

@@ -495,3 +495,26 @@ def test_gates_far_below_zero_keep_their_precision_in_the_gradients(gdn, N):
     off = ((got - want) / want).abs().max() / U
     print(f"  dh0: {float(off):.1f} roundings", flush=True)
     assert off <= 31
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [8, 16, 32])
+@pytest.mark.parametrize("T,C", [(1, 16), (6, 70), (43, 130), (64, 24)])
+def test_a_bad_last_token_leaves_the_gradients_before_it(gdn, T, C, N, dtype):
+    # x of the last token is in no other token's gradients, in neither those of A (which take the states in front of a token) nor h0's
+    x = _cuda(_draw([T, T], C, N, 1, dtype, 23 + T))
+    call = lambda v: gdn.ssm_bwd(**dict(_args(x), x=v), dy=x["dy"], h0=x["h0"], dh_T=x["dh_T"])
+    clean = call(x["x"])
+    bad = x["x"].clone()
+    bad[0, -1, 3], bad[1, -1, 5], bad[1, -1, C - 1] = float("inf"), float("nan"), -float("inf")
+    got = call(bad)
+    for k in ("dA", "dh0", "dx"):
+        assert torch.equal(got[k], clean[k]), k
+    for k in ("ddt", "dz", "dB", "dC"):
+        assert torch.equal(got[k][:, :-1], clean[k][:, :-1]), k
+    others = [c for c in range(C) if c not in (3, 5, C - 1)]
+    for k in ("ddt", "dz"):
+        assert torch.equal(got[k][..., others], clean[k][..., others]), k
+    for k in ("dD", "ddt_bias"):
+        assert torch.equal(got[k][others], clean[k][others]) and not got[k][[3, 5, C - 1]].isfinite().any(), k
