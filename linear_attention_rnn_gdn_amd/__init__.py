@@ -69,16 +69,26 @@ class GdnLinearShape(ctypes.Structure):
                 ("B", "T", "H_qk", "H_v", "d_k", "d_v", "g_fixed", "dtype", "o_dtype")]
 
 
-class GdnConvShape(ctypes.Structure):
+class _Sizes(ctypes.Structure):
+    """Sizes that tensors of one channel or one row can have, and the library
+    cannot take: refused, where ctypes by itself would keep their low 32 bits."""
+
+    def __init__(self, *sizes):
+        if any(not -1 << 31 <= n < 1 << 31 for n in sizes):
+            raise GdnError(-2, type(self).__name__)
+        super().__init__(*sizes)
+
+
+class GdnConvShape(_Sizes):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "C", "W", "ld", "n_slots", "silu", "dtype")]
 
 
-class GdnSsmShape(ctypes.Structure):
+class GdnSsmShape(_Sizes):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "T", "C", "N", "G", "n_slots", "softplus", "ld_x", "ld_dt", "ld_z", "ld_b", "ld_c", "dtype", "o_dtype")]
 
 
-class GdnVerifyShape(ctypes.Structure):
+class GdnVerifyShape(_Sizes):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "n", "V")]
 
 
