@@ -621,8 +621,10 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_shape *shape, const gdn_ssm_inputs *in, con
  *     max(p - q, 0), scaled to one (if it has no mass, p stays).
  * The walk goes on from the first child accepted.  Where there is none, the next
  * token is the lowest v at which the running sum of what is left of p passes
- * uniform[n] times its whole; -1 if p has no mass.  The tokens accepted, and
- * that one, are distributed as the target's.
+ * uniform[n] times its whole; -1 if nothing is left: p has no mass or, without
+ * draft probabilities, all of it was on refused children (whose p then add up to
+ * less than one by rounding; it happens with a chance of that size).  The tokens
+ * accepted, and that one, are distributed as the target's.
  *   B, n, V  rows, nodes per row (1..64), tokens of the vocabulary (<= 2^24)
  *   tokens, parents [B, n] int32: a node's token and its parent, an earlier
  *            node or -1; a node with another parent, or a token outside

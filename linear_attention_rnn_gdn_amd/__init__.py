@@ -1236,8 +1236,10 @@ def tree_verify(tokens, parents, target, uniform, draft=None, workspace=None, st
     uniform [B,n+1] fp32 in [0, 1): one number per node, and the last for the
     next token; draft [B,n,V] fp32: the probabilities that siblings were drawn
     from, in the order of target, or None for tokens chosen without chance.
+    Probabilities that are negative or no numbers count as zero.
     Returns int32 (last [B]: the last node accepted, -1 for none, as tree_commit
-    takes it; token [B]: the next token, -1 where the target has no mass;
+    takes it; token [B]: the next token, -1 where nothing is left to draw from:
+    the target has no mass or, without draft, none but on refused children;
     path [B,n]: the nodes accepted, in order, then -1)."""
     b, n = _leading(tokens, "tokens", 2)
     dev, v = tokens.device, _leading(target, "target", 3)[2]

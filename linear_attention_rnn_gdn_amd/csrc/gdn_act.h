@@ -36,8 +36,9 @@ template <bool ROUGH> __device__ __forceinline__ void silu_grad(float v, float &
 
 // log(1 + e^v) = max(v, 0) + log1p(e^-|v|).  With w = 1 + e rounded, log1p(e) =
 // log(w) + log1p((e - (w - 1)) / w): the rounding of w, which is all of e where
-// a step is small, is added back (e <= 1, so leaving out the division by w
-// changes that by less than 2^-25 of log(w)).
+// a step is small, is added back.  Leaving out the division by w changes that
+// by lost (w - 1) / w: at most 2^-24 of log(w), one rounding of it, as lost is
+// 2^-24 at most and (w - 1) / w no more than log(w).
 __device__ __forceinline__ float softplus(float v, float e) {
   const float w = 1.f + e, lost = e - (w - 1.f);
   return fmaf(__builtin_amdgcn_logf(w), kLn2, lost) + __builtin_elementwise_maximum(v, 0.f);

@@ -11,8 +11,10 @@
 // is read once but for the W - 1 rows before each run.
 // Measured with W = 4 in bf16, 8192 channels: 4096 tokens forward 29 us (134 MB,
 // 4.6 TB/s; a large copy reaches 5.0 to 5.2 TB/s here), gradients 50 us and 5 for
-// the pieces' sums (202 MB, 3.6 TB/s; the vector ALU is busy 67% of the time),
-// one token of 256 rows 9.8 us (34 MB), of 512 rows 13.8 us (67 MB, 4.9 TB/s).
+// the pieces' sums (202 MB, 3.6 TB/s; the vector ALU is busy 66% of the time),
+// one token of 256 rows 9.9 us (34 MB), of 512 rows 13.8 us (67 MB, 4.9 TB/s);
+// in fp32 forward 59 us (268 MB, 4.5 TB/s), gradients 91 us with the sums
+// (403 MB, 4.4 TB/s, on three waves per SIMD).
 #pragma once
 #include <type_traits>
 

@@ -14,11 +14,13 @@
 // zero, or from the sequence's own state if it begins there) and the sum of d,
 // a second carries the states from segment to segment (the decay of a whole
 // segment is e^{A sum d}), and the walks start from those.
-// Measured at 4096 tokens of 4096 channels with 16 states in bf16 (vector ALU
-// busy; its instructions per token and wave): forward 135 us = folds 58 (91%;
-// 89) + scan 12 + walks 78 (91%; 121), of which 5 N are the recurrence's own;
-// gradients 401 us = folds 104 (86%; 153) + scan 19 + walks 300 (81%; 449) +
-// sums 11.  One token of 256 rows with 4096 channels: 28 us, 143 MB, 5.0 TB/s.
+// Measured at 4096 tokens of 4096 channels with 16 states in bf16: forward
+// 135 us a call, gradients 399.  The launches' medians under the profiler, which
+// add up to more than a call without it (vector ALU busy; its instructions per
+// token and wave): forward folds 57 (91%; 89), scan 12, walks 77 (91%; 121), of
+// which 5 N are the recurrence's own; gradients folds 111 (88%; 158), scan 20,
+// walks 323 (82%; 449), sums 11.  One token of 256 rows with 4096 channels:
+// 28 us, 143 MB, 5.0 TB/s.
 #pragma once
 #include <type_traits>
 
@@ -122,9 +124,11 @@ __device__ __forceinline__ void store_states(float *p, const float (&h)[N]) {
 __device__ __forceinline__ float step_size(const SsmArgs &a, float v) { return a.softplus ? softplus(v, exp_neg_abs(v)) : v; }
 
 // Tokens asked for at once, and worked on without a branch between them, by the
-// walk (4 took 143 and 178 us instead of 140 and 176 at 4096 x 4096 and at 12
-// packed sequences, 16 states; 247 instead of 239 with 32) and by the fold of
-// the gradients, which notes states between batches, at every 4th or 8th token.
+// walk and by the fold of the gradients, which notes states between batches, at
+// every 4th or 8th token.  Batches of 4 and of 8 in the walk took, in us: 12
+// packed sequences with 16 states 178 and 175; 4096 tokens of 4096 channels in
+// bf16 97 and 94 with 8 states, 141 and 139 with 16, 246 and 238 with 32, in fp32
+// 105 and 108 with 8, 164 and 158 with 16, 270 and 270 with 32.
 constexpr int WALK_BATCH = 8, FOLD_BATCH = 4;
 
 // One wave: 64 channels of one segment.  FOLD: only the segment's end state
@@ -209,7 +213,11 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
       if constexpr (!FOLD) p.z[i] = raw(z + at * ld_z, off);
     }
   };
-  // B and C of a token, and of the next, where scalar registers hold that
+  // B and C of a token, and of the next, up to 16 words each.  (At 8 words nearly
+  // all of it stays in scalar registers.  At 16, fp32 with 16 states and bf16 with
+  // 32, it does not: 224 scalars are kept in lanes of vector registers, and 1115
+  // of 3484 and 1103 of 5107 vector instructions of the kernel, as compiled, move
+  // them there and back.)
   constexpr bool AHEAD = Row<N, TI>::WORDS <= 16;
   Row<N, TI> B, C, Bn, Cn;
   auto ask_rows = [&](Row<N, TI> &B, Row<N, TI> &C) {
@@ -305,8 +313,9 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
 // state): its four waves fold a quarter of the segments each, exchange what
 // they folded and go over them again from what enters their quarter.  Segment
 // j's own state is complete where a sequence begins in it.
-// (The scan moves two states per segment, 33 MB in 12 us at 64 segments of 4096 channels; latency bounds it.)
-constexpr int SCAN_AHEAD = 16;   // segments asked for at once
+// (The scan moves two states per segment, 33 MB in 12 us at 64 segments of 4096 channels; latency bounds it,
+// that of the flags too: they are scalar loads under a test, each waited for before the next.)
+constexpr int SCAN_AHEAD = 16;   // segments whose states and sums are asked for before they are used
 template <int N>
 __global__ __launch_bounds__(256) void ssm_scan_kernel(SsmArgs a) {
   __shared__ float folded[2][4][64];
@@ -601,8 +610,11 @@ template <int M> __device__ __forceinline__ bool reduced_writer(int lane) { retu
 // 32 states a wave takes 16, and the two waves of a channel exchange their sums
 // over states once per piece.  A piece's noted state is asked for while the
 // piece behind it is worked on: at 4096 tokens of 4096 channels with 16 states
-// this kernel takes 300 us so, and 422 where it asks for what it needs at once.
+// this kernel takes 303 us so, and took 422 where it asked for what it needed at once.
 // (Asking for the tokens' elements ahead too spills, and gained nothing.)
+// Scalar registers are short: 92 of its scalars are kept in lanes of vector
+// registers there, and 228 of the loop's 2038 vector instructions, as compiled,
+// move them.
 //
 // A lane's registers stay below 256, two waves per SIMD: with more, copies of
 // live values to accumulation registers are placed where paths join, and this

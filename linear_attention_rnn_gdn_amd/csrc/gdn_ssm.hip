@@ -16,13 +16,12 @@ namespace {
 constexpr int64_t kMaxWaves = 1ll << 25;   // a launch holds fewer than 2^32 threads
 // Segments of a forward pass: as many as give 4096 walks, four per SIMD.  At
 // 4096 tokens of 4096 channels with 16 states, and at 12 packed sequences (9925
-// tokens) of 2000 channels, 1024 walks took 364 and 425 us, 2048 190 and 235, 4096 144 and
-// 179, 8192 154 and 188 (a segment more costs its state's two passes; measured
-// with batches of 4 tokens in the walk, which has 8 now).
+// tokens) of 2000 channels, 1024 walks took 232 and 284 us, 2048 155 and 190, 4096 139 and
+// 175, 8192 152 and 189 (a segment more costs its state's two passes).
 constexpr int kWaves = 4096;
-// ... of 16 tokens or more: 8, 16, 32 and 64 took 26, 27, 36 and 60 us at 512
-// tokens of 512 channels, 48, 38, 40 and 62 at 2048 tokens of them, and 106 and
-// 66 (8 and 16) at 8192 tokens of 64.
+// ... of 16 tokens or more: 8, 16, 32 and 64 took 18, 22, 32 and 55 us at 512
+// tokens of 512 channels, 47, 37, 38 and 57 at 2048 tokens of them, and 104, 64,
+// 53 and 64 at 8192 tokens of 64.
 constexpr int kShortest = 16;
 // Segments of the gradients have 8, 16, 32 or 64 tokens, by the waves that 32
 // would give: fewer than 256, than 1536, than 8192, or more.  Measured, in us:

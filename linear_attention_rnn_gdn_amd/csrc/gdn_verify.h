@@ -27,8 +27,11 @@
 // whose sums one more workgroup per row joins to find the token's part; of a
 // small one a workgroup per row does it all, in one launch.  Latency and
 // launches bound both.  Measured: 5 nodes in a chain with draft probabilities,
-// 32003 tokens, 12.5 us a call (kernel 11.5 to 13; in three launches 19); 32
-// rows of 16 nodes without, 131072 tokens, 15.0 us a call (kernels 6.7 + 6.8; 17 MB).
+// 32003 tokens, 12.8 us a call (kernel 12.5); 32 rows of 16 nodes without,
+// 131072 tokens, 15.0 us a call (kernels 6.7 + 6.8; 17 MB).  The pass of a
+// refusal before a further child adds, at 8192, 32003, 65536 and 131072 tokens,
+// 3.0, 8.3, 16 and 30 us to one row, and 3.0, 8.5, 35 and 79 us to 32 rows that
+// each have one: it is one workgroup's, and its reads wait for each other.
 #pragma once
 #include "gdn_common.h"
 
@@ -62,6 +65,7 @@ __device__ __forceinline__ double residual(float p, float q, double t) {
 }
 
 // sum of max(p - t q, 0) over tokens lo .. hi - 1 by THREADS threads, this thread's share
+// (a token's p and then its q, each waited for before what comes next)
 template <int THREADS>
 __device__ __forceinline__ double residual_share(const float *p, const float *q, double t, int lo, int hi, int tid) {
   double s = 0.;
@@ -180,7 +184,9 @@ __device__ __forceinline__ Residual residual_of(const VerifyArgs &a, const Verif
   r.refused = __ballot(x >= lo && x < hi);
   return r;
 }
-// COUNT weights, tokens v, v + step, .. below hi (none behind it), all asked for at once
+// COUNT weights, tokens v, v + step, .. below hi (none behind it).  Without draft
+// probabilities all are asked for at once; with them each q is read under a test
+// for whether there is one, and waited for.
 template <int COUNT>
 __device__ __forceinline__ void weights(const Residual &r, int v, int step, int hi, double (&w)[COUNT]) {
   float p[COUNT], q[COUNT];

@@ -14,14 +14,21 @@ namespace {
 // One launch, a workgroup per row, for vocabularies of 2^15 tokens at most and,
 // without draft probabilities, at most 32 rows; else the sums by parts and the
 // draw in launches of their own.  Measured, one launch against several, in us
-// on the device (each launch less also saves 3 us of the host's time):
+// on the device (each launch less also saves 3 us of the host's time), 8 nodes
+// a row (4 of 512 rows of 65536 tokens), in a chain, where no refusal needs a
+// pass over the vocabulary, or a tree, half of whose nodes continue the one
+// before and half branch off any earlier one (with draft probabilities 0.3 to
+// 0.7 passes a row, and up to 4 of the row that has most):
 //   tokens                        8192          32003         65536
-//   draft,    1 row             9.5 / 14.9   13.1 / 14.5   18.9 / 15.0
-//            32 rows           10.8 / 17.2   19.8 / 20.6   33.1 / 21.9
-//           512 rows           24.3 / 30.5   55.3 / 61.1   95.8 / 85.5
-//   no draft, 1 row             7.9 /  9.4    8.4 /  9.2   12.2 /  9.4
-//            32 rows           10.7 / 10.6   11.4 / 10.5   14.6 / 10.8
-//           512 rows           22.3 / 16.4   25.5 / 24.1   41.7 / 39.6
+//   draft, chain, 1 row         9.6 / 15.1   13.1 / 14.6    19.1 / 15.1
+//                32 rows       10.7 / 17.3   20.1 / 20.6    33.4 / 22.0
+//               512 rows       24.4 / 31.1   55.5 / 60.9    96.2 / 86.0
+//   draft, tree,  1 row        10.7 / 16.2   12.1 / 13.9    19.1 / 14.8
+//                32 rows       15.6 / 21.2   29.7 / 43.4    69.5 / 66.7
+//               512 rows       33.7 / 39.2  104.6 / 103.2  153.3 / 154.8
+//   no draft, tree, 1 row       7.8 /  9.4    8.2 /  9.2    12.0 /  9.2
+//                  32 rows     10.6 / 10.6   11.3 / 10.5    14.5 / 11.1
+//                 512 rows     22.1 / 16.4   25.2 / 24.4    41.3 / 39.4
 constexpr int kRowTokens = 1 << 15, kRowRows = 32;
 static_assert(kRowTokens <= VERIFY_CHUNKS * VERIFY_CHUNK, "the sums of a row's chunks lie in LDS");
 
