@@ -308,6 +308,14 @@ __global__ __launch_bounds__(64, 2) void ssm_walk_kernel(SsmArgs a) {
   }
 }
 
+// f + 2^x h: a state carried over many tokens (the sum of d times A, in units of
+// log2(e)).  In two halves: where states grow, 2^x alone may pass fp32 while the
+// state is zero, or so small that the product does not; x / 2 is held below 128.
+__device__ __forceinline__ float carry(float x, float h, float f) {
+  const float half = __builtin_amdgcn_exp2f(fminf(0.5f * x, 127.f));
+  return fmaf(half, half * h, f);
+}
+
 // The states entering the segments (or, REV, the cotangents entering them from
 // behind, from the last one on).  A workgroup takes one (row, 64 channels,
 // state): its four waves fold a quarter of the segments each, exchange what
@@ -350,7 +358,7 @@ __global__ __launch_bounds__(256) void ssm_scan_kernel(SsmArgs a) {
 #pragma unroll
       for (int m = 0; m < SCAN_AHEAD; ++m) {
         if (k + m >= k1) break;
-        h = fresh[m] ? e[m] : fmaf(__builtin_amdgcn_exp2f(s[m] * A), h, e[m]);
+        h = fresh[m] ? e[m] : carry(s[m] * A, h, e[m]);
         sum += s[m];
         begun = begun || fresh[m];
         if (write) in[(((row * (int64_t)a.J + first + way * (k + m + 1)) * a.tiles + tile) * N + n) * 64 + lane] = h;
@@ -365,7 +373,7 @@ __global__ __launch_bounds__(256) void ssm_scan_kernel(SsmArgs a) {
   h = rev && a.dh_T ? a.dh_T[((size_t)row * a.C + c) * N + n] : 0.f;
   for (int w = 0; w < wave; ++w) {
     const float f = folded[0][w][lane];
-    h = begins[w] ? f : fmaf(__builtin_amdgcn_exp2f(folded[1][w][lane] * A), h, f);
+    h = begins[w] ? f : carry(folded[1][w][lane] * A, h, f);
   }
   pass(true);
 }

@@ -518,3 +518,30 @@ def test_a_bad_last_token_leaves_the_gradients_before_it(gdn, T, C, N, dtype):
         assert torch.equal(got[k][..., others], clean[k][..., others]), k
     for k in ("dD", "ddt_bias"):
         assert torch.equal(got[k][others], clean[k][others]) and not got[k][[3, 5, C - 1]].isfinite().any(), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [12000, 30000])
+@pytest.mark.parametrize("N", [8, 16, 32])
+def test_growing_states_that_are_zero_for_long_stay_zero(gdn, N, T):
+    # Rates above zero, no input before the last 300 tokens, no cotangent behind the first 300: over the tokens between them a
+    # state would grow by far more than fp32 holds, but there is none, forward and back.  What comes out is what calls on the 300
+    # tokens alone give, whose segments begin elsewhere.  All terms are positive, so each call is off by its roundings, relative
+    # to the value: of exponents that add up to 300 x 0.1 x 0.5 = 15 at most, 76 u of each (12 of the exponent and 64 of sums),
+    # 1140 u; of 300 tokens, 4 u each, 1200 u; of the output fewer than 60 u.  Two calls: 4800 u.
+    gen = torch.Generator().manual_seed(T + N)
+    C = 5
+    pos = lambda *s: 0.5 + torch.rand(*s, generator=gen)
+    x, dy = torch.zeros(1, T, C), torch.zeros(1, T, C)
+    x[:, -300:], dy[:, :300] = pos(1, 300, C), pos(1, 300, C)
+    all_ = dict(x=x, dt=torch.full((1, T, C), 0.1), A=0.3 + 0.2 * torch.rand(C, N, generator=gen), B=pos(1, T, 1, N), C=pos(1, T, 1, N))
+    cut = lambda lo, hi: {k: v if k == "A" else v[:, lo:hi].contiguous() for k, v in all_.items()}
+    near = lambda a, b: bool(((a - b).abs() <= 4800 * U * b).all())
+    y, h = gdn.ssm_fwd(**_cuda(all_), softplus=False)
+    y1, h1 = gdn.ssm_fwd(**_cuda(cut(T - 300, T)), softplus=False)
+    assert (y[:, :-300] == 0).all() and near(y[:, -300:], y1) and near(h, h1)
+    g = gdn.ssm_bwd(**_cuda(all_), dy=dy.cuda(), softplus=False)
+    g1 = gdn.ssm_bwd(**_cuda(cut(0, 300)), dy=dy[:, :300].contiguous().cuda(), softplus=False)
+    for k in ("dx", "dh0"):
+        assert near(g[k][:, :300] if k == "dx" else g[k], g1[k]), k
+    assert (g["dx"][:, 300:] == 0).all() and all((g[k] == 0).all() for k in ("dA", "dB", "dC", "ddt"))
